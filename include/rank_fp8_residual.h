@@ -351,6 +351,92 @@ const char *ll_kernel_name(ll_handle h, int i);
 int ll_forward_noalloc(const void *x, const void *A, const void *B, const void *Q, const float *scale,
                        int scale_mode, const void *bias, void *y, int M, int N, int K, int r, void *stream);
 
+/* ---------------------------------------------------------------------
+ * Int8 operators: the RMS norm that precedes a linear layer, with its int8
+ * output, the per-row int8 quantisation, and a linear layer whose weight is
+ * held as int8 codes with one scale per output feature.  The pages have no
+ * counterpart beyond the RMS norm and the 8-bit linears that their video
+ * transformers replace (q8-ltx-video README).  They chain: norm -> codes ->
+ * layer (bias, GELU) -> quantisation -> layer.  All three are forward only.
+ *
+ * Tensors are row-major and contiguous device memory of the current device
+ * (the layer's: the device that was current when it was created, which must
+ * also be current in its calls).  K % 16 == 0, K >= 16.  Each of these calls
+ * is asynchronous on `stream` unless it says otherwise, allocates nothing
+ * and keeps no state, so any number of them may run at once, on several
+ * streams and captured into several graphs.
+ *
+ * An int8 row stands for codes[m, k] * scale[m], codes in [-127, 127]. */
+
+/* RMS norm of M rows with the residual's addition and an int8 output:
+ *
+ *   h[m, k]     = bf16(x[m, k] + residual[m, k])   (h = x if residual is NULL)
+ *   u[m, k]     = h[m, k] * weight[k]              (u = h if weight is NULL)
+ *   rstd[m]     = 1 / sqrt(mean_k h[m, k]^2 + eps)
+ *   y[m, k]     = bf16(u[m, k] * rstd[m])
+ *   a[m]        = max_k |u[m, k]|
+ *   codes[m, k] = the integer nearest to 127 u[m, k] / a[m], ties to even
+ *   scale[m]    = a[m] * rstd[m] / 127
+ *
+ * x, residual, weight, h, y: bf16, [M, K] ([K] for weight); codes int8
+ * [M, K]; scale fp32 [M].  residual, weight, h and y may be NULL, and codes
+ * together with scale; one of y and codes must be asked for, and h only
+ * with a residual.  h may be x or residual itself (in place); no other
+ * output may overlap an input or another output.  u is the exact product
+ * (it fits binary32), and the codes are the exact rounding of the quotient:
+ * they have one right value.  A row of zeros has codes and scale 0; a row
+ * in which some u is NaN or infinite has codes 0 and scale NaN.  Sums and
+ * rstd are binary32; squares that overflow it are summed scaled, so every
+ * finite row has its norm.  eps >= 1e-30.  M == 0 is a no-op.
+ * Errors: LL_ERR_INVALID_ARG for bad sizes or eps, null / misaligned
+ * (16 bytes; scale 4) / overlapping pointers or pointers that are not memory
+ * of the current device; LL_ERR_UNSUPPORTED for K > 65536; LL_ERR_CUDA. */
+int ll_rmsnorm_i8(const void *x, const void *residual, const void *weight, float eps, int M, int K, void *h, void *y,
+                  void *codes, float *scale, void *stream);
+
+/* Per-row int8 quantisation: a[m] = max_k |x[m, k]|, codes[m, k] = the
+ * integer nearest to 127 x[m, k] / a[m] (ties to even), scale[m] = a[m] / 127.
+ * x bf16 [M, K], codes int8 [M, K], scale fp32 [M].  For activations (a row
+ * is a token) and for a dense weight (a row is an output feature).  Rows of
+ * zeros, NaN and infinities, and errors, as ll_rmsnorm_i8. */
+int ll_quantize_i8(const void *x, int M, int K, void *codes, float *scale, void *stream);
+
+/* A linear layer with an int8 weight:
+ *
+ *   y[m, n] = bf16(act(xs[m] * ws[n] * sum_k xq[m, k] wq[n, k] + bias[n]))
+ *
+ * xq, wq int8 codes ([M, K] and [N, K]; -128 is allowed), xs [M] and ws [N]
+ * fp32, bias bf16.  The sum is exact (int32). */
+typedef struct ll_i8_layer *ll_i8_handle;
+
+/* Create a layer of N output and K input features on the current device.
+ * N >= 1 and N % 8 == 0.  Device memory for the weight is allocated here.
+ * Returns NULL on error (see ll_last_error()): LL_ERR_INVALID_ARG for bad
+ * sizes, LL_ERR_UNSUPPORTED for K > 131056 (the int32 sum) or a GPU other
+ * than sm_100, LL_ERR_OOM / LL_ERR_CUDA. */
+ll_i8_handle ll_i8_create(int N, int K);
+
+/* Copy the weight into handle-owned device memory (synchronises the device;
+ * the caller may free its buffers once the call returns).  codes int8
+ * [N, K] (16-byte aligned), scale fp32 [N], finite, bias bf16 [N] or NULL.
+ * LL_ERR_INVALID_ARG as above or for a non-finite scale. */
+int ll_i8_set_weights(ll_i8_handle h, const void *codes, const float *scale, const void *bias);
+
+/* LL_EPILOGUE_NONE or LL_EPILOGUE_GELU_TANH, applied to the fp32 result
+ * before its rounding to bf16 (LL_ERR_UNSUPPORTED for GEGLU). */
+int ll_i8_set_epilogue(ll_i8_handle h, int epilogue);
+
+/* y = forward(codes, scale) for M tokens: codes int8 [M, K] and y bf16
+ * [M, N] 16-byte aligned, scale fp32 [M]; y must not overlap the inputs.
+ * A NaN scale gives a row of NaN.  M == 0 is a no-op.  LL_ERR_NOT_READY
+ * before ll_i8_set_weights. */
+int ll_i8_forward(ll_i8_handle h, const void *codes, const float *scale, void *y, int M, void *stream);
+
+/* As ll_status, ll_set_debug and ll_destroy, for an int8 layer. */
+int ll_i8_status(ll_i8_handle h);
+int ll_i8_set_debug(ll_i8_handle h, int withhold_producer, uint64_t timeout_ns);
+void ll_i8_destroy(ll_i8_handle h);
+
 #ifdef __cplusplus
 }
 #endif

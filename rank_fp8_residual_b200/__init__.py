@@ -69,6 +69,15 @@ _SIGNATURES = {
     "ll_quantize_x": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P, _P, _P]),
     "ll_plan": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                _P, _P, _P]),
+    "ll_rmsnorm_i8": (ctypes.c_int, [_P, _P, _P, ctypes.c_float, ctypes.c_int, ctypes.c_int, _P, _P, _P, _P, _P]),
+    "ll_quantize_i8": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int, _P, _P, _P]),
+    "ll_i8_create": (_P, [ctypes.c_int, ctypes.c_int]),
+    "ll_i8_set_weights": (ctypes.c_int, [_P, _P, _P, _P]),
+    "ll_i8_set_epilogue": (ctypes.c_int, [_P, ctypes.c_int]),
+    "ll_i8_forward": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, _P]),
+    "ll_i8_status": (ctypes.c_int, [_P]),
+    "ll_i8_set_debug": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_uint64]),
+    "ll_i8_destroy": (None, [_P]),
 }
 
 
@@ -257,6 +266,137 @@ def ll_plan(N: int, K: int, r: int, M: int, num_sms: int, variant: int = 0):
     if rc != LL_OK:
         raise LLError(rc, "ll_plan")
     return k.value, bt.value, ks.value
+
+
+def _buffer(t, what, dtype, *shape):
+    """Address of an argument of the int8 operators.  A tensor has to be
+    contiguous CUDA memory of that type and shape (the library sees only its
+    address); an integer address is taken as it is."""
+    if t is None or isinstance(t, int):
+        return t
+    if str(t.dtype) != dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
+        raise LLError(LL_ERR_INVALID_ARG, f"{what}: a contiguous CUDA tensor of {dtype} and shape {shape} is needed, "
+                                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def ll_rmsnorm_i8(x, residual, weight, eps: float, M: int, K: int, h, y, codes, scale, stream=None) -> None:
+    """RMS norm with the residual's addition and an int8 output:
+    h = bf16(x + residual), u = h * weight, y = bf16(u / rms(h)), codes =
+    round(127 u / max|u|) and scale = max|u| / rms(h) / 127 per row.  bf16
+    [M, K] tensors (weight [K]), codes int8 [M, K], scale float32 [M];
+    residual, weight, h, y and codes with scale may be None (see the
+    header)."""
+    M, K, b = int(M), int(K), "torch.bfloat16"
+    rc = _lib.ll_rmsnorm_i8(_buffer(x, "x", b, M, K), _buffer(residual, "residual", b, M, K),
+                            _buffer(weight, "weight", b, K), eps, M, K, _buffer(h, "h", b, M, K),
+                            _buffer(y, "y", b, M, K), _buffer(codes, "codes", "torch.int8", M, K),
+                            _buffer(scale, "scale", "torch.float32", M), _stream(stream))
+    if rc != LL_OK:
+        raise LLError(rc, "ll_rmsnorm_i8")
+
+
+def ll_quantize_i8(x, M: int, K: int, codes, scale, stream=None) -> None:
+    """Int8 codes and scale of each row of x (bf16 [M, K], device): codes int8
+    [M, K], scale float32 [M], x ~= codes * scale."""
+    M, K = int(M), int(K)
+    rc = _lib.ll_quantize_i8(_buffer(x, "x", "torch.bfloat16", M, K), M, K, _buffer(codes, "codes", "torch.int8", M, K),
+                             _buffer(scale, "scale", "torch.float32", M), _stream(stream))
+    if rc != LL_OK:
+        raise LLError(rc, "ll_quantize_i8")
+
+
+def ll_i8_create(N: int, K: int) -> int:
+    h = _lib.ll_i8_create(int(N), int(K))
+    if not h:
+        raise LLError(_lib.ll_last_error(), "ll_i8_create")
+    return h
+
+
+def ll_i8_set_weights(h: int, codes, scale, bias=None) -> None:
+    rc = _lib.ll_i8_set_weights(h, _addr(codes), _addr(scale), _addr(bias))
+    if rc != LL_OK:
+        raise LLError(rc, "ll_i8_set_weights")
+
+
+def ll_i8_set_epilogue(h: int, epilogue: int) -> None:
+    rc = _lib.ll_i8_set_epilogue(h, int(epilogue))
+    if rc != LL_OK:
+        raise LLError(rc, "ll_i8_set_epilogue")
+
+
+def ll_i8_forward(h: int, codes, scale, y, M: int, stream=None) -> None:
+    rc = _lib.ll_i8_forward(h, _addr(codes), _addr(scale), _addr(y), int(M), _stream(stream))
+    if rc != LL_OK:
+        raise LLError(rc, "ll_i8_forward")
+
+
+def ll_i8_status(h: int) -> int:
+    return _lib.ll_i8_status(h)
+
+
+def ll_i8_set_debug(h: int, withhold_producer: bool, timeout_ns: int) -> None:
+    rc = _lib.ll_i8_set_debug(h, int(bool(withhold_producer)), int(timeout_ns))
+    if rc != LL_OK:
+        raise LLError(rc, "ll_i8_set_debug")
+
+
+def ll_i8_destroy(h: int) -> None:
+    _lib.ll_i8_destroy(h)
+
+
+class Int8LinearLayer:
+    """Owns one int8 layer: y = bf16(act(scale[m] * w_scale[n] * (codes
+    w_codes^T) + bias)).  ``forward(codes, scale)`` takes the int8 codes [M, K]
+    and float32 scale [M] of ll_rmsnorm_i8 or ll_quantize_i8 and returns a new
+    bf16 tensor [M, N] (or ``out``)."""
+
+    def __init__(self, N: int, K: int, epilogue: int = LL_EPILOGUE_NONE):
+        self.handle = None
+        self.N, self.K = int(N), int(K)
+        self.handle = ll_i8_create(N, K)
+        if epilogue != LL_EPILOGUE_NONE:
+            ll_i8_set_epilogue(self.handle, epilogue)
+
+    def set_weights(self, codes, scale, bias=None):
+        """codes int8 [N, K], scale float32 [N], bias bf16 [N] or None (CUDA)."""
+        ll_i8_set_weights(self.handle, _buffer(codes, "codes", "torch.int8", self.N, self.K),
+                          _buffer(scale, "scale", "torch.float32", self.N),
+                          _buffer(bias, "bias", "torch.bfloat16", self.N))
+
+    @classmethod
+    def from_dense(cls, W, bias=None, epilogue: int = LL_EPILOGUE_NONE):
+        """A layer from a dense CUDA bf16 weight [out, in], quantised per
+        output feature by ll_quantize_i8."""
+        import torch
+        N, K = W.shape
+        codes = torch.empty(N, K, dtype=torch.int8, device=W.device)
+        scale = torch.empty(N, dtype=torch.float32, device=W.device)
+        ll_quantize_i8(W.contiguous(), N, K, codes, scale)
+        layer = cls(N, K, epilogue)
+        layer.set_weights(codes, scale, bias)
+        return layer
+
+    def forward(self, codes, scale, out=None, stream=None):
+        M = codes.shape[0]
+        if out is None:
+            import torch
+            out = torch.empty(M, self.N, dtype=torch.bfloat16, device=codes.device)
+        ll_i8_forward(self.handle, _buffer(codes, "codes", "torch.int8", M, self.K),
+                      _buffer(scale, "scale", "torch.float32", M), _buffer(out, "out", "torch.bfloat16", M, self.N),
+                      M, stream)
+        return out
+
+    def close(self):
+        if self.handle:
+            ll_i8_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 class LiteLinearLayer:

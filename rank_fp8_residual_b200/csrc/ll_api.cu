@@ -1923,3 +1923,7 @@ extern "C" int ll_forward_noalloc(const void* x, const void* A, const void* B, c
   const int rc = forward_noalloc(x, A, B, Q, scale, scale_mode, bias, y, M, N, K, r, static_cast<cudaStream_t>(stream));
   return rc == LL_OK ? LL_OK : fail(rc);
 }
+
+// ===========================================================================
+// The int8 operators: ll_rmsnorm_i8, ll_quantize_i8 and the int8 layer.
+#include "ll_i8_host.cuh"

@@ -1,0 +1,287 @@
+// Host side of the int8 operators of include/rank_fp8_residual.h: the row
+// kernels (ll_rows_i8.cuh) and the int8 layer (ll_i8.cuh).  Included by
+// ll_api.cu, whose helpers it uses.
+#pragma once
+
+#include <new>
+
+#include "ll_i8.cuh"
+#include "ll_rows_i8.cuh"
+
+// The int8 layer.  Its forwards change nothing here, on the host or on the
+// device (except the status word after a timeout), so they may run on any
+// streams at once.
+struct ll_i8_layer {
+  int N = 0, K = 0, device = 0, num_sms = 0;
+  bool ready = false, has_bias = false;
+  int8_t* W = nullptr;       // [N, K]
+  float* scale = nullptr;    // [N]
+  uint16_t* bias = nullptr;  // [N]
+  int* status = nullptr;
+  int epilogue = LL_EPILOGUE_NONE;
+  int withhold = 0;
+  uint64_t timeout_ns = 2000000000ull;
+};
+
+namespace {
+
+int current_device_sms(int* dev, int* sms) {
+  if (cudaGetDevice(dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess) {
+    cudaGetLastError();
+    return LL_ERR_CUDA;
+  }
+  return LL_OK;
+}
+
+// Makes a device current for a scope.
+struct DeviceScope {
+  int prev = -1;
+  explicit DeviceScope(int dev) {
+    if (cudaGetDevice(&prev) != cudaSuccess || prev == dev || cudaSetDevice(dev) != cudaSuccess) prev = -1;
+  }
+  ~DeviceScope() {
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+};
+
+int launch_rows_i8(const llk::RowsParams& p, int sms, cudaStream_t st) {
+  using namespace llk;
+  const int nv = p.K / 8;
+  int threads = std::min(1024, (nv + 31) / 32 * 32);
+  const int blocks = std::min(p.M, sms * 16);
+  int c = (nv + threads - 1) / threads;
+  if (c == 1)
+    ll_rows_i8_kernel<1><<<blocks, threads, 0, st>>>(p);
+  else if (c == 2)
+    ll_rows_i8_kernel<2><<<blocks, threads, 0, st>>>(p);
+  else if (c <= 4)
+    ll_rows_i8_kernel<4><<<blocks, threads, 0, st>>>(p);
+  else
+    ll_rows_i8_kernel<8><<<blocks, threads, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? LL_OK : LL_ERR_CUDA;
+}
+
+void free_i8(ll_i8_layer* h) {
+  cudaFree(h->W);
+  cudaFree(h->scale);
+  cudaFree(h->bias);
+  cudaFree(h->status);
+  delete h;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ll_rmsnorm_i8(const void* x, const void* residual, const void* weight, float eps, int M, int K, void* h, void* y,
+                  void* codes, float* scale, void* stream) {
+  g_last_error = LL_OK;
+  if (M < 0 || K < 16 || K % 16 != 0 || !std::isfinite(eps) || eps < 1e-30f) return fail(LL_ERR_INVALID_ARG);
+  if (K > llk::kRowsMaxK) return fail(LL_ERR_UNSUPPORTED);
+  if ((codes == nullptr) != (scale == nullptr) || (!codes && !y) || (h && !residual)) return fail(LL_ERR_INVALID_ARG);
+  if (M == 0) return LL_OK;
+  if (!x) return fail(LL_ERR_INVALID_ARG);
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(h, 16) || !aligned(y, 16) ||
+      !aligned(codes, 16) || !aligned(scale, 4))
+    return fail(LL_ERR_INVALID_ARG);
+  const size_t n = static_cast<size_t>(M) * K;
+  // Each output against every input and every other output; h may be x or
+  // residual itself.
+  const void* outs[4] = {h, y, codes, scale};
+  const size_t out_bytes[4] = {2 * n, 2 * n, n, 4 * static_cast<size_t>(M)};
+  const void* ins[3] = {x, residual, weight};
+  const size_t in_bytes[3] = {2 * n, 2 * n, 2 * static_cast<size_t>(K)};
+  for (int i = 0; i < 4; ++i) {
+    if (!outs[i]) continue;
+    for (int j = 0; j < 3; ++j) {
+      if (!ins[j] || (i == 0 && j < 2 && outs[i] == ins[j])) continue;
+      if (overlaps(outs[i], out_bytes[i], ins[j], in_bytes[j])) return fail(LL_ERR_INVALID_ARG);
+    }
+    for (int j = 0; j < i; ++j)
+      if (outs[j] && overlaps(outs[i], out_bytes[i], outs[j], out_bytes[j])) return fail(LL_ERR_INVALID_ARG);
+  }
+  int dev = 0, sms = 0;
+  if (current_device_sms(&dev, &sms) != LL_OK) return fail(LL_ERR_CUDA);
+  for (const void* p : {x, residual, weight, static_cast<const void*>(h), static_cast<const void*>(y),
+                        static_cast<const void*>(codes), static_cast<const void*>(scale)})
+    if (p && !is_device_ptr_on(p, dev)) return fail(LL_ERR_INVALID_ARG);
+  llk::RowsParams rp{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(residual),
+                     static_cast<const uint16_t*>(weight), static_cast<uint16_t*>(h), static_cast<uint16_t*>(y),
+                     static_cast<int8_t*>(codes), scale, eps, M, K, 1};
+  const int rc = launch_rows_i8(rp, sms, static_cast<cudaStream_t>(stream));
+  return rc == LL_OK ? LL_OK : fail(rc);
+}
+
+int ll_quantize_i8(const void* x, int M, int K, void* codes, float* scale, void* stream) {
+  g_last_error = LL_OK;
+  if (M < 0 || K < 16 || K % 16 != 0) return fail(LL_ERR_INVALID_ARG);
+  if (K > llk::kRowsMaxK) return fail(LL_ERR_UNSUPPORTED);
+  if (M == 0) return LL_OK;
+  if (!x || !codes || !scale || !aligned(x, 16) || !aligned(codes, 16) || !aligned(scale, 4))
+    return fail(LL_ERR_INVALID_ARG);
+  const size_t n = static_cast<size_t>(M) * K, ns = 4 * static_cast<size_t>(M);
+  if (overlaps(codes, n, x, 2 * n) || overlaps(scale, ns, x, 2 * n) || overlaps(scale, ns, codes, n))
+    return fail(LL_ERR_INVALID_ARG);
+  int dev = 0, sms = 0;
+  if (current_device_sms(&dev, &sms) != LL_OK) return fail(LL_ERR_CUDA);
+  if (!is_device_ptr_on(x, dev) || !is_device_ptr_on(codes, dev) || !is_device_ptr_on(scale, dev))
+    return fail(LL_ERR_INVALID_ARG);
+  llk::RowsParams rp{static_cast<const uint16_t*>(x), nullptr, nullptr, nullptr, nullptr, static_cast<int8_t*>(codes),
+                     scale, 0.f, M, K, 0};
+  const int rc = launch_rows_i8(rp, sms, static_cast<cudaStream_t>(stream));
+  return rc == LL_OK ? LL_OK : fail(rc);
+}
+
+ll_i8_handle ll_i8_create(int N, int K) {
+  g_last_error = LL_OK;
+  if (N < 1 || N % 8 != 0 || K < 16 || K % 16 != 0) {
+    fail(LL_ERR_INVALID_ARG);
+    return nullptr;
+  }
+  if (K > llk::kI8MaxK) {
+    fail(LL_ERR_UNSUPPORTED);
+    return nullptr;
+  }
+  int dev = 0, sms = 0, major = 0, minor = 0;
+  if (current_device_sms(&dev, &sms) != LL_OK ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
+    cudaGetLastError();
+    fail(LL_ERR_CUDA);
+    return nullptr;
+  }
+  if (major != 10 || minor != 0) {
+    fail(LL_ERR_UNSUPPORTED);
+    return nullptr;
+  }
+  ll_i8_layer* h = new (std::nothrow) ll_i8_layer();
+  if (!h) {
+    fail(LL_ERR_OOM);
+    return nullptr;
+  }
+  h->N = N;
+  h->K = K;
+  h->device = dev;
+  h->num_sms = sms;
+  if (cudaMalloc(&h->W, static_cast<size_t>(N) * K) != cudaSuccess ||
+      cudaMalloc(&h->scale, sizeof(float) * N) != cudaSuccess ||
+      cudaMalloc(&h->bias, sizeof(uint16_t) * N) != cudaSuccess || cudaMalloc(&h->status, sizeof(int)) != cudaSuccess) {
+    cudaGetLastError();
+    free_i8(h);
+    fail(LL_ERR_OOM);
+    return nullptr;
+  }
+  if (cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+    cudaGetLastError();
+    free_i8(h);
+    fail(LL_ERR_CUDA);
+    return nullptr;
+  }
+  return h;
+}
+
+int ll_i8_set_weights(ll_i8_handle h, const void* codes, const float* scale, const void* bias) {
+  g_last_error = LL_OK;
+  if (!h || !codes || !scale || !aligned(codes, 16) || !aligned(scale, 4) || !aligned(bias, 2))
+    return fail(LL_ERR_INVALID_ARG);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(LL_ERR_CUDA);
+  }
+  if (dev != h->device || !is_device_ptr_on(codes, dev) || !is_device_ptr_on(scale, dev) ||
+      (bias && !is_device_ptr_on(bias, dev)))
+    return fail(LL_ERR_INVALID_ARG);
+  const size_t sb = sizeof(float) * h->N;
+  float* host = static_cast<float*>(std::malloc(sb));
+  if (!host) return fail(LL_ERR_OOM);
+  // A forward still running reads the weights that this call replaces.
+  bool ok = cudaDeviceSynchronize() == cudaSuccess &&
+            cudaMemcpy(host, scale, sb, cudaMemcpyDeviceToHost) == cudaSuccess;
+  bool finite = true;
+  for (int n = 0; ok && n < h->N; ++n) finite &= std::isfinite(host[n]);
+  std::free(host);
+  if (ok && !finite) return fail(LL_ERR_INVALID_ARG);
+  if (ok) {
+    h->ready = false;
+    ok = cudaMemcpy(h->W, codes, static_cast<size_t>(h->N) * h->K, cudaMemcpyDeviceToDevice) == cudaSuccess &&
+         cudaMemcpy(h->scale, scale, sb, cudaMemcpyDeviceToDevice) == cudaSuccess &&
+         (bias ? cudaMemcpy(h->bias, bias, sizeof(uint16_t) * h->N, cudaMemcpyDeviceToDevice) == cudaSuccess : true) &&
+         cudaDeviceSynchronize() == cudaSuccess;
+  }
+  if (!ok) {
+    cudaGetLastError();
+    return fail(LL_ERR_CUDA);
+  }
+  h->has_bias = bias != nullptr;
+  h->ready = true;
+  return LL_OK;
+}
+
+int ll_i8_set_epilogue(ll_i8_handle h, int epilogue) {
+  g_last_error = LL_OK;
+  if (!h || epilogue < LL_EPILOGUE_NONE || epilogue > LL_EPILOGUE_GEGLU_TANH) return fail(LL_ERR_INVALID_ARG);
+  if (epilogue == LL_EPILOGUE_GEGLU_TANH) return fail(LL_ERR_UNSUPPORTED);
+  h->epilogue = epilogue;
+  return LL_OK;
+}
+
+int ll_i8_forward(ll_i8_handle h, const void* codes, const float* scale, void* y, int M, void* stream) {
+  g_last_error = LL_OK;
+  if (!h || M < 0) return fail(LL_ERR_INVALID_ARG);
+  if (!h->ready) return fail(LL_ERR_NOT_READY);
+  if (M == 0) return LL_OK;
+  if (!codes || !scale || !y || !aligned(codes, 16) || !aligned(scale, 4) || !aligned(y, 16))
+    return fail(LL_ERR_INVALID_ARG);
+  const size_t yb = 2 * static_cast<size_t>(M) * h->N;
+  if (overlaps(y, yb, codes, static_cast<size_t>(M) * h->K) || overlaps(y, yb, scale, 4 * static_cast<size_t>(M)))
+    return fail(LL_ERR_INVALID_ARG);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(LL_ERR_CUDA);
+  }
+  if (dev != h->device || !is_device_ptr_on(codes, dev) || !is_device_ptr_on(scale, dev) || !is_device_ptr_on(y, dev))
+    return fail(LL_ERR_INVALID_ARG);
+  const dim3 grid((h->N + 63) / 64, (M + 63) / 64);
+  llk::ll_i8_simple_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
+      static_cast<const int8_t*>(codes), scale, h->W, h->scale, h->has_bias ? h->bias : nullptr,
+      static_cast<uint16_t*>(y), M, h->N, h->K, h->epilogue == LL_EPILOGUE_GELU_TANH);
+  if (cudaGetLastError() != cudaSuccess) return fail(LL_ERR_CUDA);
+  return LL_OK;
+}
+
+int ll_i8_status(ll_i8_handle h) {
+  g_last_error = LL_OK;
+  if (!h) return fail(LL_ERR_INVALID_ARG);
+  const DeviceScope on(h->device);
+  int v = 0;
+  if (cudaDeviceSynchronize() != cudaSuccess ||
+      cudaMemcpy(&v, h->status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(LL_ERR_CUDA);
+  }
+  if (v == 0) return LL_OK;
+  cudaMemset(h->status, 0, sizeof(int));
+  cudaDeviceSynchronize();
+  return LL_ERR_DEVICE_TIMEOUT;
+}
+
+int ll_i8_set_debug(ll_i8_handle h, int withhold_producer, uint64_t timeout_ns) {
+  g_last_error = LL_OK;
+  if (!h || timeout_ns == 0) return fail(LL_ERR_INVALID_ARG);
+  h->withhold = withhold_producer ? 1 : 0;
+  h->timeout_ns = timeout_ns;
+  return LL_OK;
+}
+
+void ll_i8_destroy(ll_i8_handle h) {
+  if (!h) return;
+  const DeviceScope on(h->device);
+  cudaDeviceSynchronize();
+  free_i8(h);
+  cudaGetLastError();
+}
+
+}  // extern "C"
