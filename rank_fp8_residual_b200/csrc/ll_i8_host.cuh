@@ -13,11 +13,12 @@
 // streams at once.
 struct ll_i8_layer {
   int N = 0, K = 0, device = 0, num_sms = 0;
-  bool ready = false, has_bias = false;
-  int8_t* W = nullptr;       // [N, K]
-  float* scale = nullptr;    // [N]
-  uint16_t* bias = nullptr;  // [N]
+  bool ready = false;
+  int8_t* W = nullptr;   // [N, K]
+  float2* sb = nullptr;  // [N_pad] (scale, bias), zeros behind the last feature
+  int N_pad = 0;         // room for a tile of 256 features that starts at the last one
   int* status = nullptr;
+  int clusters[llk::kIsMaxSplit + 1] = {};  // co-resident clusters of that many CTAs of the streaming kernel
   int epilogue = LL_EPILOGUE_NONE;
   int withhold = 0;
   uint64_t timeout_ns = 2000000000ull;
@@ -62,10 +63,119 @@ int launch_rows_i8(const llk::RowsParams& p, int sms, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? LL_OK : LL_ERR_CUDA;
 }
 
+using I8Fn = void (*)(llk::I8Params);
+using I8StreamFn = void (*)(llk::I8StreamParams);
+I8Fn kernel_i8(int epilogue) {
+  return epilogue == LL_EPILOGUE_GELU_TANH ? llk::ll_i8_kernel<llk::kActGelu> : llk::ll_i8_kernel<llk::kActNone>;
+}
+I8StreamFn kernel_i8_stream(int epilogue) {
+  return epilogue == LL_EPILOGUE_GELU_TANH ? llk::ll_i8_stream_kernel<llk::kActGelu>
+                                           : llk::ll_i8_stream_kernel<llk::kActNone>;
+}
+
+// Per device: the kernels' shared-memory limits, and how many clusters of
+// the streaming kernel fit at once.
+bool setup_i8(ll_i8_layer* h) {
+  using namespace llk;
+  for (int e : {LL_EPILOGUE_NONE, LL_EPILOGUE_GELU_TANH})
+    if (cudaFuncSetAttribute(kernel_i8(e), cudaFuncAttributeMaxDynamicSharedMemorySize, i8_smem_bytes()) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel_i8_stream(e), cudaFuncAttributeMaxDynamicSharedMemorySize, kIsRing + 1280) !=
+            cudaSuccess)
+      return false;
+  for (int s = 2; s <= kIsMaxSplit; ++s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = static_cast<unsigned>(s);
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(h->num_sms, s);
+    cfg.blockDim = dim3(kIsThreads);
+    cfg.dynamicSmemBytes = kIsRing + 1280;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&h->clusters[s], kernel_i8_stream(LL_EPILOGUE_NONE), &cfg) != cudaSuccess)
+      return false;
+  }
+  h->clusters[1] = h->num_sms;
+  return true;
+}
+
+constexpr int kI8StreamMaxM = 256;
+
+int launch_i8_stream(const ll_i8_layer* h, const void* codes, const float* scale, void* y, int M, cudaStream_t st) {
+  using namespace llk;
+  constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  I8StreamParams p;
+  p.Mt = (M + 15) / 16 * 16;
+  if (!make_map(&p.tm_x, codes, kU8, M, h->K, h->K, 128, p.Mt, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&p.tm_w, h->W, kU8, h->N, h->K, h->K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    return LL_ERR_CUDA;
+  p.sx = scale;
+  p.sb = h->sb;
+  p.y = static_cast<uint16_t*>(y);
+  p.M = M;
+  p.N = h->N;
+  p.K = h->K;
+  p.tmem_cols = next_pow2_ge32(p.Mt);
+  p.withhold = h->withhold;
+  p.watch = Watch{h->status, h->timeout_ns};
+  const int tiles = (h->N + 127) / 128, steps = (h->K + 127) / 128;
+  int s = 1;
+  while (s < std::min(kIsMaxSplit, steps) && tiles <= h->clusters[s + 1]) ++s;
+  p.steps = (steps + s - 1) / s;
+  p.splits = (steps + p.steps - 1) / p.steps;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = static_cast<unsigned>(p.splits);
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(tiles, p.splits);
+  cfg.blockDim = dim3(kIsThreads);
+  cfg.dynamicSmemBytes = is_smem_bytes(p.Mt);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel_i8_stream(h->epilogue), p) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
+}
+
+int launch_i8(const ll_i8_layer* h, const void* codes, const float* scale, void* y, int M, cudaStream_t st) {
+  using namespace llk;
+  constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  I8Params p;
+  p.fn = 256;
+  if (!make_map(&p.tm_x, codes, kU8, M, h->K, h->K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&p.tm_w, h->W, kU8, h->N, h->K, h->K, 128, p.fn / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&p.tm_y, y, kBF16, M, h->N, 2ull * h->N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    return LL_ERR_CUDA;
+  p.sx = scale;
+  p.sb = h->sb;
+  p.M = M;
+  p.N = h->N;
+  p.K = h->K;
+  p.n_ttiles = (M + 255) / 256;
+  p.n_ftiles = (h->N + p.fn - 1) / p.fn;
+  p.withhold = h->withhold;
+  p.watch = Watch{h->status, h->timeout_ns};
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(2 * std::min(p.n_ttiles * p.n_ftiles, h->num_sms / 2));
+  cfg.blockDim = dim3(kI8Threads);
+  cfg.dynamicSmemBytes = i8_smem_bytes();
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel_i8(h->epilogue), p) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
+}
+
 void free_i8(ll_i8_layer* h) {
   cudaFree(h->W);
-  cudaFree(h->scale);
-  cudaFree(h->bias);
+  cudaFree(h->sb);
   cudaFree(h->status);
   delete h;
 }
@@ -164,15 +274,16 @@ ll_i8_handle ll_i8_create(int N, int K) {
   h->K = K;
   h->device = dev;
   h->num_sms = sms;
+  h->N_pad = (N + 511) / 256 * 256;
   if (cudaMalloc(&h->W, static_cast<size_t>(N) * K) != cudaSuccess ||
-      cudaMalloc(&h->scale, sizeof(float) * N) != cudaSuccess ||
-      cudaMalloc(&h->bias, sizeof(uint16_t) * N) != cudaSuccess || cudaMalloc(&h->status, sizeof(int)) != cudaSuccess) {
+      cudaMalloc(&h->sb, sizeof(float2) * h->N_pad) != cudaSuccess || cudaMalloc(&h->status, sizeof(int)) != cudaSuccess) {
     cudaGetLastError();
     free_i8(h);
     fail(LL_ERR_OOM);
     return nullptr;
   }
-  if (cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  if (!setup_i8(h) || !encode_fn() || cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess ||
+      cudaDeviceSynchronize() != cudaSuccess) {
     cudaGetLastError();
     free_i8(h);
     fail(LL_ERR_CUDA);
@@ -205,16 +316,15 @@ int ll_i8_set_weights(ll_i8_handle h, const void* codes, const float* scale, con
   if (ok && !finite) return fail(LL_ERR_INVALID_ARG);
   if (ok) {
     h->ready = false;
-    ok = cudaMemcpy(h->W, codes, static_cast<size_t>(h->N) * h->K, cudaMemcpyDeviceToDevice) == cudaSuccess &&
-         cudaMemcpy(h->scale, scale, sb, cudaMemcpyDeviceToDevice) == cudaSuccess &&
-         (bias ? cudaMemcpy(h->bias, bias, sizeof(uint16_t) * h->N, cudaMemcpyDeviceToDevice) == cudaSuccess : true) &&
-         cudaDeviceSynchronize() == cudaSuccess;
+    ok = cudaMemcpy(h->W, codes, static_cast<size_t>(h->N) * h->K, cudaMemcpyDeviceToDevice) == cudaSuccess;
+    llk::ll_i8_scale_bias_kernel<<<(h->N_pad + 255) / 256, 256>>>(scale, static_cast<const uint16_t*>(bias), h->sb, h->N,
+                                                                 h->N_pad);
+    ok = ok && cudaGetLastError() == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
   }
   if (!ok) {
     cudaGetLastError();
     return fail(LL_ERR_CUDA);
   }
-  h->has_bias = bias != nullptr;
   h->ready = true;
   return LL_OK;
 }
@@ -244,12 +354,10 @@ int ll_i8_forward(ll_i8_handle h, const void* codes, const float* scale, void* y
   }
   if (dev != h->device || !is_device_ptr_on(codes, dev) || !is_device_ptr_on(scale, dev) || !is_device_ptr_on(y, dev))
     return fail(LL_ERR_INVALID_ARG);
-  const dim3 grid((h->N + 63) / 64, (M + 63) / 64);
-  llk::ll_i8_simple_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
-      static_cast<const int8_t*>(codes), scale, h->W, h->scale, h->has_bias ? h->bias : nullptr,
-      static_cast<uint16_t*>(y), M, h->N, h->K, h->epilogue == LL_EPILOGUE_GELU_TANH);
-  if (cudaGetLastError() != cudaSuccess) return fail(LL_ERR_CUDA);
-  return LL_OK;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int rc = M <= kI8StreamMaxM ? launch_i8_stream(h, codes, scale, y, M, st) : launch_i8(h, codes, scale, y, M, st);
+  if (rc != LL_OK) cudaGetLastError();
+  return rc == LL_OK ? LL_OK : fail(rc);
 }
 
 int ll_i8_status(ll_i8_handle h) {

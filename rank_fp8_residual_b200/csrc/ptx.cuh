@@ -192,6 +192,16 @@ __device__ __forceinline__ void tmem_ld32_wait(uint32_t taddr, uint32_t (&r)[32]
       : "r"(taddr)
       : "memory");
 }
+// Load 16 consecutive columns of this thread's lane and wait.
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : LLK_R8(0), LLK_R8(8)
+      : "r"(taddr)
+      : "memory");
+}
 // Two 16-column loads (from two TMEM addresses) with one wait.
 __device__ __forceinline__ void tmem_ld16x2_wait(uint32_t ta, uint32_t (&r)[16], uint32_t tb, uint32_t (&s)[16]) {
   asm volatile(
@@ -318,6 +328,11 @@ __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t cluster_addr) {
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(cluster_addr)
                : "memory");
+  return v;
+}
+__device__ __forceinline__ int2 ld_shared_cluster_i2(uint32_t cluster_addr) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(cluster_addr) : "memory");
   return v;
 }
 __device__ __forceinline__ void st_shared_cluster_u32(uint32_t cluster_addr, uint32_t v) {

@@ -322,6 +322,25 @@ def test_layer_refusals():
     assert torch.equal(layer.forward(xq, xs), want)  # refused calls changed nothing
 
 
+@pytest.mark.parametrize("M,N", [(1, 264), (40, 2048), (200, 136), (600, 520), (3000, 2048)])
+def test_withheld_loads_time_out_and_the_layer_recovers(M, N):
+    """Every device-side wait is bounded: with loads withheld the waits run
+    out, the status tells so and is cleared, and the layer works again."""
+    xq, xs, wq, ws, b = _product_inputs(M, 1040, N, 33)
+    layer = _layer(wq, ws, b)
+    want = _forward(layer, xq, xs)
+    x, s = xq.cuda(), xs.cuda()
+    ll.ll_i8_set_debug(layer.handle, True, 1_000_000)
+    layer.forward(x, s)
+    torch.cuda.synchronize()
+    assert ll.ll_i8_status(layer.handle) == ll.LL_ERR_DEVICE_TIMEOUT
+    assert ll.ll_i8_status(layer.handle) == ll.LL_OK
+    ll.ll_i8_set_debug(layer.handle, False, 2_000_000_000)
+    assert torch.equal(_forward(layer, xq, xs), want)
+    ref, size = i8ref.product(xq, xs, wq, ws, b, False)
+    i8ref.check_y(want, ref, i8ref.PRODUCT_TOL * size)
+
+
 def test_two_layers_and_two_streams_at_once():
     """Forwards of one layer on two streams, another layer beside them, and a
     captured graph of each replayed at the same time."""
