@@ -112,8 +112,10 @@ def _addr(t):
 
 def _stream(s):
     if s is None:
+        # torch.cuda.current_stream().cuda_stream without the Stream object
+        # (0.2 against 3.2 us, which a one-token call would feel)
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -268,16 +270,26 @@ def ll_plan(N: int, K: int, r: int, M: int, num_sms: int, variant: int = 0):
     return k.value, bt.value, ks.value
 
 
-def _buffer(t, what, dtype, *shape):
+_BF16 = _INT8 = _F32 = None
+
+
+def _load_dtypes():
+    """torch's types, once (importing this package does not import torch)."""
+    global _BF16, _INT8, _F32
+    import torch
+    _BF16, _INT8, _F32 = torch.bfloat16, torch.int8, torch.float32
+
+
+def _buffer(t, what, dtype, shape):
     """Address of an argument of the int8 operators.  A tensor has to be
     contiguous CUDA memory of that type and shape (the library sees only its
     address); an integer address is taken as it is."""
-    if t is None or isinstance(t, int):
+    if t is None or type(t) is int:
         return t
-    if str(t.dtype) != dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
-        raise LLError(LL_ERR_INVALID_ARG, f"{what}: a contiguous CUDA tensor of {dtype} and shape {shape} is needed, "
-                                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise LLError(LL_ERR_INVALID_ARG, f"{what}: a contiguous CUDA tensor of {dtype} and shape {shape} is needed, "
+                                      f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def ll_rmsnorm_i8(x, residual, weight, eps: float, M: int, K: int, h, y, codes, scale, stream=None) -> None:
@@ -287,11 +299,14 @@ def ll_rmsnorm_i8(x, residual, weight, eps: float, M: int, K: int, h, y, codes, 
     [M, K] tensors (weight [K]), codes int8 [M, K], scale float32 [M];
     residual, weight, h, y and codes with scale may be None (see the
     header)."""
-    M, K, b = int(M), int(K), "torch.bfloat16"
-    rc = _lib.ll_rmsnorm_i8(_buffer(x, "x", b, M, K), _buffer(residual, "residual", b, M, K),
-                            _buffer(weight, "weight", b, K), eps, M, K, _buffer(h, "h", b, M, K),
-                            _buffer(y, "y", b, M, K), _buffer(codes, "codes", "torch.int8", M, K),
-                            _buffer(scale, "scale", "torch.float32", M), _stream(stream))
+    if _BF16 is None:
+        _load_dtypes()
+    M, K, b = int(M), int(K), _BF16
+    mk = (M, K)
+    rc = _lib.ll_rmsnorm_i8(_buffer(x, "x", b, mk), _buffer(residual, "residual", b, mk),
+                            _buffer(weight, "weight", b, (K,)), eps, M, K, _buffer(h, "h", b, mk),
+                            _buffer(y, "y", b, mk), _buffer(codes, "codes", _INT8, mk),
+                            _buffer(scale, "scale", _F32, (M,)), _stream(stream))
     if rc != LL_OK:
         raise LLError(rc, "ll_rmsnorm_i8")
 
@@ -299,9 +314,12 @@ def ll_rmsnorm_i8(x, residual, weight, eps: float, M: int, K: int, h, y, codes, 
 def ll_quantize_i8(x, M: int, K: int, codes, scale, stream=None) -> None:
     """Int8 codes and scale of each row of x (bf16 [M, K], device): codes int8
     [M, K], scale float32 [M], x ~= codes * scale."""
+    if _BF16 is None:
+        _load_dtypes()
     M, K = int(M), int(K)
-    rc = _lib.ll_quantize_i8(_buffer(x, "x", "torch.bfloat16", M, K), M, K, _buffer(codes, "codes", "torch.int8", M, K),
-                             _buffer(scale, "scale", "torch.float32", M), _stream(stream))
+    mk = (M, K)
+    rc = _lib.ll_quantize_i8(_buffer(x, "x", _BF16, mk), M, K, _buffer(codes, "codes", _INT8, mk),
+                             _buffer(scale, "scale", _F32, (M,)), _stream(stream))
     if rc != LL_OK:
         raise LLError(rc, "ll_quantize_i8")
 
@@ -360,9 +378,9 @@ class Int8LinearLayer:
 
     def set_weights(self, codes, scale, bias=None):
         """codes int8 [N, K], scale float32 [N], bias bf16 [N] or None (CUDA)."""
-        ll_i8_set_weights(self.handle, _buffer(codes, "codes", "torch.int8", self.N, self.K),
-                          _buffer(scale, "scale", "torch.float32", self.N),
-                          _buffer(bias, "bias", "torch.bfloat16", self.N))
+        _load_dtypes()
+        ll_i8_set_weights(self.handle, _buffer(codes, "codes", _INT8, (self.N, self.K)),
+                          _buffer(scale, "scale", _F32, (self.N,)), _buffer(bias, "bias", _BF16, (self.N,)))
 
     @classmethod
     def from_dense(cls, W, bias=None, epilogue: int = LL_EPILOGUE_NONE):
@@ -378,13 +396,14 @@ class Int8LinearLayer:
         return layer
 
     def forward(self, codes, scale, out=None, stream=None):
+        if _BF16 is None:
+            _load_dtypes()
         M = codes.shape[0]
         if out is None:
             import torch
-            out = torch.empty(M, self.N, dtype=torch.bfloat16, device=codes.device)
-        ll_i8_forward(self.handle, _buffer(codes, "codes", "torch.int8", M, self.K),
-                      _buffer(scale, "scale", "torch.float32", M), _buffer(out, "out", "torch.bfloat16", M, self.N),
-                      M, stream)
+            out = torch.empty(M, self.N, dtype=_BF16, device=codes.device)
+        ll_i8_forward(self.handle, _buffer(codes, "codes", _INT8, (M, self.K)), _buffer(scale, "scale", _F32, (M,)),
+                      _buffer(out, "out", _BF16, (M, self.N)), M, stream)
         return out
 
     def close(self):
