@@ -56,15 +56,48 @@ __device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
-// gelu(v) = v / 2 (1 + tanh(z)) = v / (1 + exp(-2 z)), z = sqrt(2 / pi) (v + 0.044715 v^3).
+// Two binary32 values at once (the packed multiply-add of sm_100).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float ex2(float v) {
+  float d;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
+  return d;
+}
+__device__ __forceinline__ float rcp(float v) {
+  float d;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
+  return d;
+}
+
+// Two neighbouring outputs of a token from their sums: sm is the token's
+// scale, s = (scale, scale, bias, bias) of the two features.  GELU:
+// v / 2 (1 + tanh(z)) = v / (1 + exp(-2 z)), z = sqrt(2 / pi) (v + 0.044715 v^3);
+// exp(-2 z) as a power of two: -2 z log2(e) = v (-2.3022082 - 0.10294324 v^2).
 template <int kAct>
-__device__ __forceinline__ float i8_act(float v) {
+__device__ __forceinline__ uint32_t i8_out2(int a0, int a1, float sm, const float4& s) {
+  float2 v = fma2(mul2(make_float2(s.x, s.y), make_float2(sm, sm)),
+                  make_float2(static_cast<float>(a0), static_cast<float>(a1)), make_float2(s.z, s.w));
   if constexpr (kAct == kActGelu) {
-    const float z2 = 1.5957691216057308f * fmaf(0.044715f * v, v * v, v);
-    return __fdividef(v, 1.f + __expf(-z2));
-  } else {
-    return v;
+    const float2 t = mul2(v, fma2(mul2(v, v), make_float2(-0.10294324f, -0.10294324f),
+                                  make_float2(-2.3022082f, -2.3022082f)));
+    v = mul2(v, make_float2(rcp(1.f + ex2(t.x)), rcp(1.f + ex2(t.y))));
   }
+  return pack_bf16x2(v.x, v.y);
 }
 
 // ==================================================== many tokens: CTA pairs
@@ -73,7 +106,7 @@ struct I8Params {
   CUtensorMap tm_w;  // s8 wq [N, K]  box {128, fn / 2}, 128B swizzle
   CUtensorMap tm_y;  // bf16 y [M, N] box {32, 32},      64B swizzle
   const float* sx;       // [M]
-  const float2* sb;      // [N rounded up] (scale, bias) of each feature
+  const float4* sb;      // [N rounded up / 2] (scale, scale, bias, bias) of two features
   int M, N, K;
   int fn;                  // features per tile: a multiple of 32, 32..256
   int n_ttiles, n_ftiles;  // tiles of 256 tokens and fn features
@@ -258,14 +291,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
         const int f = ft * fn + 32 * c;
         uint32_t v[32];
         tmem_ld32_wait(acc + 32u * c, v);
-        const float4* sb4 = reinterpret_cast<const float4*>(p.sb + f);  // two features per float4
+        const float4* sb4 = p.sb + f / 2;
         uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float4 s = __ldg(sb4 + i);
-          w[i] = pack_bf16x2(i8_act<kAct>(fmaf(s.x * sm, static_cast<float>(static_cast<int>(v[2 * i])), s.y)),
-                             i8_act<kAct>(fmaf(s.z * sm, static_cast<float>(static_cast<int>(v[2 * i + 1])), s.w)));
-        }
+        for (int i = 0; i < 16; ++i)
+          w[i] = i8_out2<kAct>(static_cast<int>(v[2 * i]), static_cast<int>(v[2 * i + 1]), sm, __ldg(sb4 + i));
         if (lane == 0) tma_store_wait_read<1>();
         __syncwarp();
         uint8_t* st = stg + eb * (32 * 64);
@@ -307,7 +337,7 @@ struct I8StreamParams {
   CUtensorMap tm_x;  // s8 xq [M, K] box {128, Mt},  128B swizzle
   CUtensorMap tm_w;  // s8 wq [N, K] box {128, 128}, 128B swizzle
   const float* sx;   // [M]
-  const float2* sb;  // [N rounded up] (scale, bias) of each feature
+  const float4* sb;  // [N rounded up / 2] (scale, scale, bias, bias) of two features
   uint16_t* y;       // [M, N] bf16 bits
   int M, N, K;
   int Mt;            // MMA N: tokens padded to a multiple of 16, 16..256
@@ -457,22 +487,23 @@ __global__ void __launch_bounds__(kIsThreads, 1) ll_i8_stream_kernel(const __gri
           acc.y += v.y;
         }
     }
-    const float sm = __ldg(p.sx + m);
-    const float4 s = __ldg(reinterpret_cast<const float4*>(p.sb + f0 + c));
     *reinterpret_cast<uint32_t*>(p.y + static_cast<size_t>(m) * p.N + f0 + c) =
-        pack_bf16x2(i8_act<kAct>(fmaf(s.x * sm, static_cast<float>(acc.x), s.y)),
-                    i8_act<kAct>(fmaf(s.z * sm, static_cast<float>(acc.y), s.w)));
+        i8_out2<kAct>(acc.x, acc.y, __ldg(p.sx + m), __ldg(p.sb + (f0 + c) / 2));
   }
   __syncwarp();
   if (p.splits > 1) cluster_sync();  // no CTA leaves while a peer still reads its sums
 }
 
-// (scale, bias) of each feature as the epilogues read them, zeros behind the
-// last feature (a tile may end there).
+// (scale, scale, bias, bias) of two features as the epilogues read them, zeros
+// behind the last feature (a tile may end there).
 __global__ void ll_i8_scale_bias_kernel(const float* __restrict__ scale, const uint16_t* __restrict__ bias,
-                                        float2* __restrict__ sb, int N, int N_pad) {
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < N_pad; i += gridDim.x * blockDim.x)
-    sb[i] = i < N ? make_float2(scale[i], bias ? bf16_bits_to_float(bias[i]) : 0.f) : make_float2(0.f, 0.f);
+                                        float4* __restrict__ sb, int N, int N_pad) {
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < N_pad / 2; i += gridDim.x * blockDim.x) {
+    const bool in = 2 * i < N;  // N is even
+    const float2 s = in ? make_float2(scale[2 * i], scale[2 * i + 1]) : make_float2(0.f, 0.f);
+    sb[i] = in && bias ? make_float4(s.x, s.y, bf16_bits_to_float(bias[2 * i]), bf16_bits_to_float(bias[2 * i + 1]))
+                       : make_float4(s.x, s.y, 0.f, 0.f);
+  }
 }
 
 }  // namespace llk

@@ -15,7 +15,7 @@ struct ll_i8_layer {
   int N = 0, K = 0, device = 0, num_sms = 0;
   bool ready = false;
   int8_t* W = nullptr;   // [N, K]
-  float2* sb = nullptr;  // [N_pad] (scale, bias), zeros behind the last feature
+  float4* sb = nullptr;  // [N_pad / 2] (scale, scale, bias, bias), zeros behind the last feature
   int N_pad = 0;         // room for a tile of 256 features that starts at the last one
   int* status = nullptr;
   int clusters[llk::kIsMaxSplit + 1] = {};  // co-resident clusters of that many CTAs of the streaming kernel
@@ -296,7 +296,7 @@ ll_i8_handle ll_i8_create(int N, int K) {
   h->num_sms = sms;
   h->N_pad = (N + 511) / 256 * 256;
   if (cudaMalloc(&h->W, static_cast<size_t>(N) * K) != cudaSuccess ||
-      cudaMalloc(&h->sb, sizeof(float2) * h->N_pad) != cudaSuccess || cudaMalloc(&h->status, sizeof(int)) != cudaSuccess) {
+      cudaMalloc(&h->sb, sizeof(float4) * (h->N_pad / 2)) != cudaSuccess || cudaMalloc(&h->status, sizeof(int)) != cudaSuccess) {
     cudaGetLastError();
     free_i8(h);
     fail(LL_ERR_OOM);
@@ -337,7 +337,7 @@ int ll_i8_set_weights(ll_i8_handle h, const void* codes, const float* scale, con
   if (ok) {
     h->ready = false;
     ok = cudaMemcpy(h->W, codes, static_cast<size_t>(h->N) * h->K, cudaMemcpyDeviceToDevice) == cudaSuccess;
-    llk::ll_i8_scale_bias_kernel<<<(h->N_pad + 255) / 256, 256>>>(scale, static_cast<const uint16_t*>(bias), h->sb, h->N,
+    llk::ll_i8_scale_bias_kernel<<<(h->N_pad / 2 + 255) / 256, 256>>>(scale, static_cast<const uint16_t*>(bias), h->sb, h->N,
                                                                  h->N_pad);
     ok = ok && cudaGetLastError() == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
   }
