@@ -37,22 +37,93 @@ __host__ __device__ __forceinline__ constexpr uint32_t idesc_i8(int m, int n) {
          | (static_cast<uint32_t>(m >> 4) << 24);   // M / 16
 }
 
+// MMAs, commits and tile loads are issued by one lane of a warp whose control
+// flow stays uniform: with the descriptors in warp-uniform registers an MMA of
+// 256 x 64 issues every 45 cycles with a commit after every four (65 with a
+// barrier poll too); from inside an `if (lane == 0)` it took 110, whatever its
+// size.  `one` is elect_one()'s.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
 __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
+                                       uint32_t accumulate, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one)
       : "memory");
 }
 __device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+                                            uint32_t accumulate, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one_pair(uint64_t* bar, uint16_t cta_mask, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "h"(cta_mask), "r"(one)
+      : "memory");
+}
+
+__device__ __forceinline__ void expect_one(uint64_t* bar, uint32_t bytes, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(bytes), "r"(one)
+      : "memory");
+}
+// Tile loads into shared memory, completing on a barrier of this CTA, or (pair)
+// on one of either CTA of the pair, given by its cluster address.
+__device__ __forceinline__ void load_2d_one(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1,
+                                            uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::
+          "r"(dst),
+      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void load_3d_one(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
+                                            uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];\n\t}" ::"r"(dst),
+      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void load_2d_pair_one(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1,
+                                                 uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4}], [%2];\n\t}" ::"r"(dst),
+      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void load_3d_pair_one(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1,
+                                                 int c2, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+      "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4, %5}], [%2];\n\t}" ::"r"(dst),
+      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(one)
       : "memory");
 }
 
@@ -100,71 +171,95 @@ __device__ __forceinline__ uint32_t i8_out2(int a0, int a1, float sm, const floa
   return pack_bf16x2(v.x, v.y);
 }
 
+// Outputs of one feature (this lane's; s, b its scale and bias) for the 16
+// tokens from m0 on: a warp's lanes are 32 neighbouring features, 64 bytes of
+// a token's row.
+template <int kAct>
+__device__ __forceinline__ void i8_store_tokens(const uint32_t (&v)[16], int m0, int M, int N, int f, float s, float b,
+                                                const float* __restrict__ sx, uint16_t* __restrict__ y) {
+  if (f >= N) return;
+  uint16_t* d = y + static_cast<size_t>(m0) * N + f;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    if (m0 + i >= M) break;
+    const bool two = m0 + i + 1 < M;
+    const float a0 = __ldg(sx + m0 + i), a1 = two ? __ldg(sx + m0 + i + 1) : 0.f;
+    const uint32_t w = i8_out2<kAct>(static_cast<int>(v[i]), static_cast<int>(v[i + 1]), s, make_float4(a0, a1, b, b));
+    d[static_cast<size_t>(i) * N] = static_cast<uint16_t>(w);
+    if (two) d[static_cast<size_t>(i + 1) * N] = static_cast<uint16_t>(w >> 16);
+  }
+}
+
 // ==================================================== many tokens: CTA pairs
+//
+// A tile is 256 rows of one operand (a) x up to 256 of the other (b), of one
+// CTA pair: each CTA stages its 128 rows of a and half of b's per 128-deep K
+// step and holds the accumulator of its rows of a x all of b's, twice, so that a
+// tile's epilogue runs under the next tile's products.  kSwap = false: a is the
+// tokens, b the features; a thread of the epilogue owns a token, and the outputs
+// go through shared memory and TMA stores.  kSwap = true: a is the features, b
+// the tokens (batches whose tokens would fill tiles of 256 badly); a thread
+// owns a feature and stores it token by token.
 struct I8Params {
-  CUtensorMap tm_x;  // s8 xq [M, K]  box {128, 128},    128B swizzle
-  CUtensorMap tm_w;  // s8 wq [N, K]  box {128, fn / 2}, 128B swizzle
-  CUtensorMap tm_y;  // bf16 y [M, N] box {32, 32},      64B swizzle
+  CUtensorMap tm_x;  // s8 xq [M, K]  box {128, rows}, 128B swizzle
+  CUtensorMap tm_w;  // s8 weight panels [K / 128][N][128]  box {128, rows, 1}, 128B swizzle
+  CUtensorMap tm_y;  // bf16 y [M, N] box {32, 32}, 64B swizzle (kSwap = false)
   const float* sx;       // [M]
   const float4* sb;      // [N rounded up / 2] (scale, scale, bias, bias) of two features
+  uint16_t* y;           // [M, N] bf16 bits
   int M, N, K;
-  int fn;                  // features per tile: a multiple of 32, 32..256
-  int n_ttiles, n_ftiles;  // tiles of 256 tokens and fn features
-  int withhold;            // debug: the producers issue nothing, so every consumer's wait runs out
+  int na, nb;            // tiles of a and b
+  int w;                 // rows of b per tile: a multiple of 32, 64..256
+  int withhold;          // debug: the producers issue nothing, so every consumer's wait runs out
   Watch watch;
 };
 
 constexpr int kI8Ring = 192 * 1024;
-constexpr int kI8MaxStages = 8;
+constexpr int kI8MaxStages = 9;
 constexpr int kI8EpiWarps = 8;
 constexpr int kI8Threads = 32 * (2 + kI8EpiWarps);
 constexpr int kI8Stage = 2 * 32 * 64;  // per epilogue warp: two 32 x 32 bf16 staging buffers
-constexpr int kI8Group = 8;            // token tiles per raster group
+constexpr int kI8Group = 8;            // tiles of a per raster group
 
-__host__ __device__ constexpr int i8_stage_bytes(int fn) { return 128 * 128 + fn * 64; }
-__host__ __device__ constexpr int i8_stages(int fn) {
-  return kI8Ring / i8_stage_bytes(fn) < kI8MaxStages ? kI8Ring / i8_stage_bytes(fn) : kI8MaxStages;
+// A ring slot: 128 rows of a and w / 2 of b, 128 codes each.
+__host__ __device__ constexpr int i8_slot_bytes(int w) { return 16384 + w * 64; }
+__host__ __device__ constexpr int i8_stages(int w) {
+  return kI8Ring / i8_slot_bytes(w) < kI8MaxStages ? kI8Ring / i8_slot_bytes(w) : kI8MaxStages;
 }
 __host__ __device__ constexpr int i8_smem_bytes() { return kI8Ring + kI8EpiWarps * kI8Stage + 1024 + 256; }
 
-__device__ __forceinline__ void i8_tile_coords(const I8Params& p, int T, int& tt, int& ft) {
-  const int per_group = kI8Group * p.n_ftiles;
+// Groups of kI8Group tiles of a, a fastest: the tiles in flight share their
+// rows of both operands in L2.
+__device__ __forceinline__ void i8_tile_coords(const I8Params& p, int T, int& ta, int& tb) {
+  const int per_group = kI8Group * p.nb;
   const int g = T / per_group;
   const int first = g * kI8Group;
-  const int gsize = min(kI8Group, p.n_ttiles - first);
+  const int gsize = min(kI8Group, p.na - first);
   const int idx = T - g * per_group;
-  ft = idx / gsize;
-  tt = first + idx % gsize;
+  tb = idx / gsize;
+  ta = first + idx % gsize;
 }
 
-// A tile is 256 tokens x fn features of one CTA pair: each CTA stages its 128
-// token rows and its fn / 2 feature rows per 128-deep K step and holds the
-// accumulator of its tokens x all fn features, twice, so that a tile's
-// epilogue runs under the next tile's products.  Warps: 0 TMA producer, 1
-// MMA issuer (leader) and TMEM allocator, 2-9 epilogue (lane quadrant
-// warp % 4; two warps share a quadrant and take alternate 32-column chunks).
-template <int kAct>
+// Warps: 0 TMA producer, 1 MMA issuer (leader) and TMEM allocator, 2-9
+// epilogue (lane quadrant warp % 4; two warps share a quadrant and take
+// alternate chunks of columns).
+template <int kAct, bool kSwap>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     ll_i8_kernel(const __grid_constant__ I8Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = align1024(smem_raw);
   uint8_t* epi = ring + kI8Ring;
   uint64_t* full = reinterpret_cast<uint64_t*>(epi + kI8EpiWarps * kI8Stage);  // leader: both CTAs' loads landed
-  uint64_t* empty = full + kI8MaxStages;                                      // both: the MMAs are done with the slot
-  uint64_t* tfull = empty + kI8MaxStages;                                     // both: accumulator buffer ready
+  uint64_t* empty = full + kI8MaxStages;                                         // both: the MMAs are done with the slot
+  uint64_t* tfull = empty + kI8MaxStages;                                        // both: accumulator buffer ready
   uint64_t* tempty = tfull + 2;                                               // leader: both CTAs' epilogues done
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const int rank = static_cast<int>(cluster_ctarank());
   const bool leader = rank == 0;
-  const int fn = p.fn;
-  const int sb = i8_stage_bytes(fn);
-  const int ns = i8_stages(fn);
   const int nS = (p.K + 127) / 128;  // K steps of 128 (a step past K loads as zeros)
-  const int tiles = p.n_ttiles * p.n_ftiles;
-  const int cid = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kI8MaxStages; ++s) {
@@ -179,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     fence_mbar_init();
     tma_prefetch_desc(&p.tm_x);
     tma_prefetch_desc(&p.tm_w);
-    tma_prefetch_desc(&p.tm_y);
+    if (!kSwap) tma_prefetch_desc(&p.tm_y);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -190,86 +285,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   tc_fence_after();
   pdl_launch_dependents();
   const uint32_t tbase = *tmem_slot;
+  const int pid = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+  const int tiles = p.na * p.nb;
+  const int w = p.w, slot_bytes = i8_slot_bytes(w), stages = i8_stages(w);
 
   if (warp == 0) {
     // ------------------------------------------- TMA producer (both CTAs)
-    if (lane == 0) {
-      const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
-      int slot = 0;
-      uint32_t ph = 0;
-      bool ok = !p.withhold, issued = false;
+    const uint32_t one = elect_one();
+    const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0), ring0 = smem_u32(ring);
+    int slot = 0, ta, tb;
+    uint32_t ph = 0;
+    bool ok = !p.withhold;
+    const int lap = min(stages, nS);
+    auto load_x = [&](int slot, int s) {
+      if (kSwap)
+        load_2d_pair_one(ring0 + slot * slot_bytes + 16384, &p.tm_x, full0 + 8u * slot, s * 128, tb * w + (w / 2) * rank, one);
+      else
+        load_2d_pair_one(ring0 + slot * slot_bytes, &p.tm_x, full0 + 8u * slot, s * 128, ta * 256 + 128 * rank, one);
+    };
+    auto load_w = [&](int slot, int s) {
+      if (leader) expect_one(&full[slot], 2u * slot_bytes, one);
+      if (kSwap)
+        load_3d_pair_one(ring0 + slot * slot_bytes, &p.tm_w, full0 + 8u * slot, 0, ta * 256 + 128 * rank, s, one);
+      else
+        load_3d_pair_one(ring0 + slot * slot_bytes + 16384, &p.tm_w, full0 + 8u * slot, 0, tb * w + (w / 2) * rank, s, one);
+    };
+    if (ok) {
       // The weight rows of the ring's first lap come before the wait.
-      const int lap = min(ns, nS);
-      if (ok) {
-        int tt, ft;
-        i8_tile_coords(p, cid, tt, ft);
-        for (int s = 0; s < lap; ++s) {
-          if (leader) mbar_arrive_expect_tx(&full[s], 2u * sb);
-          tma_load_2d_pair(ring + s * sb + 16384, &p.tm_w, full0 + 8u * s, s * 128, ft * fn + (fn / 2) * static_cast<int>(rank));
+      i8_tile_coords(p, pid, ta, tb);
+      for (int s = 0; s < lap; ++s) load_w(s, s);
+    }
+    pdl_wait_primary();
+    for (int T = pid; T < tiles && ok; T += pairs) {
+      i8_tile_coords(p, T, ta, tb);
+      for (int s = 0; s < nS; ++s) {
+        if (T != pid || s >= lap) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], ph ^ 1, p.watch, kErrTimeoutProducer));
+          if (!ok) break;
+          load_w(slot, s);
         }
-        issued = true;
+        load_x(slot, s);
+        if (++slot == stages) { slot = 0; ph ^= 1; }
       }
-      pdl_wait_primary();
-      for (int T = cid; T < tiles && ok; T += pairs) {
-        int tt, ft;
-        i8_tile_coords(p, T, tt, ft);
-        const int t0 = tt * 256 + 128 * static_cast<int>(rank);
-        const int f0 = ft * fn + (fn / 2) * static_cast<int>(rank);
-        for (int s = 0; s < nS; ++s) {
-          const bool first = T == cid && s < lap;
-          const uint32_t bar = full0 + 8u * slot;
-          uint8_t* dst = ring + slot * sb;
-          if (!first) {
-            if (!mbar_wait(&empty[slot], ph ^ 1, p.watch, kErrTimeoutProducer)) { ok = false; break; }
-            if (leader) mbar_arrive_expect_tx(&full[slot], 2u * sb);
-            tma_load_2d_pair(dst + 16384, &p.tm_w, bar, s * 128, f0);
-          }
-          tma_load_2d_pair(dst, &p.tm_x, bar, s * 128, t0);
-          if (++slot == ns) { slot = 0; ph ^= 1; }
-        }
-      }
-      if (!ok && issued) {
-        // Loads already issued must land before the CTA exits; they
-        // complete on leader barriers whose other arrivals may never come
-        // now, so wait a bounded settle time far above any load latency.
-        const uint64_t c0 = clock_cycles();
-        while (clock_cycles() - c0 < 400000ull) {  // >= 200 us at any clock up to 2 GHz
-        }
+    }
+    if (!ok && !p.withhold) {
+      // Loads already issued must land before the CTA exits; they
+      // complete on leader barriers whose other arrivals may never come
+      // now, so wait a bounded settle time far above any load latency.
+      const uint64_t c0 = clock_cycles();
+      while (clock_cycles() - c0 < 400000ull) {  // >= 200 us at any clock up to 2 GHz
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // --------------------------------------------- MMA issuer (leader)
       pdl_wait_primary();
-      const uint32_t id = idesc_i8(256, fn);
+      const uint32_t one = elect_one();
+      const uint32_t id = idesc_i8(256, w);
+      const uint64_t da0 = sdesc_kmajor_sw128(smem_u32(ring)), db0 = sdesc_kmajor_sw128(smem_u32(ring) + 16384);
       int slot = 0, it = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int T = cid; T < tiles && ok; T += pairs, ++it) {
+      for (int T = pid; T < tiles && ok; T += pairs, ++it) {
         const int buf = it & 1;
-        if (!mbar_wait_cl(&tempty[buf], ((it >> 1) & 1) ^ 1, p.watch, kErrTimeoutMma)) break;
-        tc_fence_after();
+        ok = __all_sync(0xffffffffu, mbar_wait_cl(&tempty[buf], ((it >> 1) & 1) ^ 1, p.watch, kErrTimeoutMma));
         const uint32_t d = tbase + 256u * buf;
-        for (int s = 0; s < nS; ++s) {
-          if (!mbar_wait_cl(&full[slot], ph, p.watch, kErrTimeoutMma)) { ok = false; break; }
+        for (int s = 0; s < nS && ok; ++s) {
+          ok = __all_sync(0xffffffffu, mbar_wait_cl(&full[slot], ph, p.watch, kErrTimeoutMma));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t base = smem_u32(ring + slot * sb);
-          const uint64_t dx = sdesc_kmajor_sw128(base);
-          const uint64_t dw = sdesc_kmajor_sw128(base + 16384);
+          const uint64_t da = da0 + static_cast<uint64_t>(slot * (slot_bytes >> 4));
+          const uint64_t db = db0 + static_cast<uint64_t>(slot * (slot_bytes >> 4));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_i8_pair(d, dx + 2 * kk, dw + 2 * kk, id, (s | kk) != 0 ? 1u : 0u);
-          tc_commit_pair(&empty[slot], 0x3);
-          if (++slot == ns) { slot = 0; ph ^= 1; }
+          for (int kk = 0; kk < 4; ++kk) mma_i8_pair(d, da + 2 * kk, db + 2 * kk, id, (s | kk) != 0 ? 1u : 0u, one);
+          commit_one_pair(&empty[slot], 0x3, one);
+          if (++slot == stages) { slot = 0; ph ^= 1; }
         }
-        if (ok) tc_commit_pair(&tfull[buf], 0x3);
+        if (ok) commit_one_pair(&tfull[buf], 0x3, one);
       }
       // No MMA may still run when TMEM is released.
-      tc_commit_pair(drain, 0x1);
-      mbar_wait_drain(drain, 0, p.watch);
+      commit_one_pair(drain, 0x1, one);
+      if (one) mbar_wait_drain(drain, 0, p.watch);
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    // TMEM lane = token row of this CTA; column = feature of the tile.
+    // TMEM lane = row of a of this CTA; column = row of b.
     pdl_wait_primary();
     const int q = warp & 3, half = (warp - 2) >> 2;
     uint8_t* stg = epi + (warp - 2) * kI8Stage;
@@ -277,39 +378,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     const uint32_t tempty_leader = mapa_shared(smem_u32(&tempty[0]), 0);
     const int sw = (lane >> 1) & 3;  // 64-byte swizzle phase of this lane's staging row
     int it = 0, eb = 0;
-    for (int T = cid; T < tiles; T += pairs, ++it) {
-      int tt, ft;
-      i8_tile_coords(p, T, tt, ft);
-      const int buf = it & 1;
-      const int trow = tt * 256 + 128 * static_cast<int>(rank) + 32 * q;
-      const int tok = trow + lane;
-      const float sm = tok < p.M ? __ldg(p.sx + tok) : 0.f;
+    for (int T = pid; T < tiles; T += pairs, ++it) {
+      int ta, tb;
+      i8_tile_coords(p, T, ta, tb);
+      const int b0 = tb * w, buf = it & 1;
+      const int row0 = ta * 256 + 128 * rank + 32 * q;
+      const int row = row0 + lane;
+      float sm = 0.f, bias = 0.f;  // kSwap: scale and bias of the feature; else the token's scale
+      if (kSwap) {
+        if (row < p.N) {
+          const float4 s2 = __ldg(p.sb + row / 2);
+          sm = row & 1 ? s2.y : s2.x;
+          bias = row & 1 ? s2.w : s2.z;
+        }
+      } else if (row < p.M) {
+        sm = __ldg(p.sx + row);
+      }
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], (it >> 1) & 1, p.watch, kErrTimeoutEpilogue))) break;
       tc_fence_after();
       const uint32_t acc = tl + 256u * buf;
-      for (int c = half; c < fn / 32; c += 2) {
-        const int f = ft * fn + 32 * c;
-        uint32_t v[32];
-        tmem_ld32_wait(acc + 32u * c, v);
-        const float4* sb4 = p.sb + f / 2;
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          w[i] = i8_out2<kAct>(static_cast<int>(v[2 * i]), static_cast<int>(v[2 * i + 1]), sm, __ldg(sb4 + i));
-        if (lane == 0) tma_store_wait_read<1>();
-        __syncwarp();
-        uint8_t* st = stg + eb * (32 * 64);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(st + lane * 64 + 16 * (j ^ sw)) =
-              make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (trow < p.M && f < p.N) tma_store_2d(&p.tm_y, st, f, trow);
-          tma_store_commit();
+      if constexpr (kSwap) {
+        for (int c = 16 * half; c < w && b0 + c < p.M; c += 32) {
+          uint32_t v[16];
+          tmem_ld16_wait(acc + c, v);
+          i8_store_tokens<kAct>(v, b0 + c, p.M, p.N, row, sm, bias, p.sx, p.y);
         }
-        eb ^= 1;
+      } else {
+        for (int c = 32 * half; c < w; c += 64) {
+          const int f = b0 + c;
+          uint32_t v[32];
+          tmem_ld32_wait(acc + c, v);
+          const float4* sb4 = p.sb + f / 2;
+          uint32_t o[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            o[i] = i8_out2<kAct>(static_cast<int>(v[2 * i]), static_cast<int>(v[2 * i + 1]), sm, __ldg(sb4 + i));
+          if (lane == 0) tma_store_wait_read<1>();
+          __syncwarp();
+          uint8_t* st = stg + eb * (32 * 64);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(st + lane * 64 + 16 * (j ^ sw)) =
+                make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < p.M && f < p.N) tma_store_2d(&p.tm_y, st, f, row0);
+            tma_store_commit();
+          }
+          eb ^= 1;
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -320,7 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
           mbar_arrive_cluster(tempty_leader + 8u * buf);
       }
     }
-    if (lane == 0) tma_store_wait<0>();
+    if (!kSwap && lane == 0) tma_store_wait<0>();
   }
 
   tc_fence_before();
@@ -335,7 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 // ============================================ few tokens: streaming the weight
 struct I8StreamParams {
   CUtensorMap tm_x;  // s8 xq [M, K] box {128, Mt},  128B swizzle
-  CUtensorMap tm_w;  // s8 wq [N, K] box {128, 128}, 128B swizzle
+  CUtensorMap tm_w;  // s8 weight panels [K / 128][N][128] box {128, 128, 1}, 128B swizzle
   const float* sx;   // [M]
   const float4* sb;  // [N rounded up / 2] (scale, scale, bias, bias) of two features
   uint16_t* y;       // [M, N] bf16 bits
@@ -344,31 +462,38 @@ struct I8StreamParams {
   int tmem_cols;     // power of two >= Mt, at least 32
   int splits;        // CTAs of a cluster that share a tile's K steps
   int steps;         // K steps of 128 per split
+  int stages;        // ring slots
   int withhold;
   Watch watch;
 };
 
-constexpr int kIsThreads = 192;  // 0 TMA producer, 1 MMA issuer and TMEM allocator, 2-5 epilogue
-constexpr int kIsRing = 208 * 1024;
+constexpr int kIsEpiWarps = 8;
+constexpr int kIsThreads = 32 * (2 + kIsEpiWarps);  // 0 TMA producer, 1 MMA issuer and TMEM allocator, 2-9 epilogue
 constexpr int kIsMaxStages = 12;
 constexpr int kIsMaxSplit = 8;
+// The small ring leaves room for a second CTA on the SM: the next kernel's,
+// whose weight loads then start under this kernel's end.
+constexpr int kIsRingSmall = 108 * 1024, kIsRingLarge = 208 * 1024;
 
 __host__ __device__ constexpr int is_stage_bytes(int Mt) { return 16384 + Mt * 128; }
-__host__ __device__ constexpr int is_stages(int Mt) {
-  return kIsRing / is_stage_bytes(Mt) < kIsMaxStages ? kIsRing / is_stage_bytes(Mt) : kIsMaxStages;
+__host__ __device__ constexpr int is_stages(int Mt, int ring) {
+  return ring / is_stage_bytes(Mt) < kIsMaxStages ? ring / is_stage_bytes(Mt) : kIsMaxStages;
 }
-__host__ __device__ constexpr int is_smem_bytes(int Mt) { return is_stages(Mt) * is_stage_bytes(Mt) + 1024 + 256; }
+__host__ __device__ constexpr int is_smem_bytes(int Mt, int ring) {
+  return is_stages(Mt, ring) * is_stage_bytes(Mt) + 1024 + 256;
+}
 
 // One CTA (or a cluster that splits K) per tile of 128 features x all tokens:
 // the weight is read once from HBM, features on the MMA's M side, tokens on
-// its N side.  The int32 sums go through shared memory ([token][feature]), and
-// the CTAs of a cluster add them over distributed shared memory, each for
-// every splits-th token.
+// its N side.  Without a split the outputs go straight from TMEM to global
+// memory (a warp's lanes are 32 features of a token).  With one the int32 sums
+// go through shared memory ([token][feature]), and the CTAs of the cluster add
+// them over distributed shared memory, each for every splits-th token.
 template <int kAct>
 __global__ void __launch_bounds__(kIsThreads, 1) ll_i8_stream_kernel(const __grid_constant__ I8StreamParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = align1024(smem_raw);
-  const int sb = is_stage_bytes(p.Mt), ns = is_stages(p.Mt);
+  const int sb = is_stage_bytes(p.Mt), ns = p.stages;
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + ns * sb);
   uint64_t* empty = full + kIsMaxStages;
   uint64_t* acc_full = empty + kIsMaxStages;
@@ -393,7 +518,7 @@ __global__ void __launch_bounds__(kIsThreads, 1) ll_i8_stream_kernel(const __gri
     if (!p.withhold)
       for (int i = 0; i < min(ns, n); ++i) {
         mbar_arrive_expect_tx(&full[i], sb);
-        tma_load_2d(ring + i * sb, &p.tm_w, &full[i], (s0 + i) * 128, f0);
+        tma_load_3d(ring + i * sb, &p.tm_w, &full[i], 0, f0, s0 + i);
       }
     tma_prefetch_desc(&p.tm_x);
   }
@@ -410,52 +535,62 @@ __global__ void __launch_bounds__(kIsThreads, 1) ll_i8_stream_kernel(const __gri
   pdl_wait_primary();
 
   if (warp == 0) {
-    if (lane == 0 && !p.withhold) {
-      for (int i = 0; i < min(ns, n); ++i) tma_load_2d(ring + i * sb + 16384, &p.tm_x, &full[i], (s0 + i) * 128, 0);
+    if (!p.withhold) {
+      const uint32_t one = elect_one();
+      const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(&full[0]);
+      for (int i = 0; i < min(ns, n); ++i)
+        load_2d_one(ring0 + i * sb + 16384, &p.tm_x, full0 + 8u * i, (s0 + i) * 128, 0, one);
       int slot = 0, i = ns;
       uint32_t ph = 0;
       for (; i < n; ++i) {
-        if (!mbar_wait(&empty[slot], ph, p.watch, kErrTimeoutProducer)) { ok = false; break; }
-        mbar_arrive_expect_tx(&full[slot], sb);
-        tma_load_2d(ring + slot * sb, &p.tm_w, &full[slot], (s0 + i) * 128, f0);
-        tma_load_2d(ring + slot * sb + 16384, &p.tm_x, &full[slot], (s0 + i) * 128, 0);
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], ph, p.watch, kErrTimeoutProducer));
+        if (!ok) break;
+        expect_one(&full[slot], sb, one);
+        load_3d_one(ring0 + slot * sb, &p.tm_w, full0 + 8u * slot, 0, f0, s0 + i, one);
+        load_2d_one(ring0 + slot * sb + 16384, &p.tm_x, full0 + 8u * slot, (s0 + i) * 128, 0, one);
         if (++slot == ns) { slot = 0; ph ^= 1; }
       }
       if (!ok)  // let every load already issued land before the CTA can exit
         for (int j = max(0, i - ns); j < i; ++j) mbar_wait_drain(&full[j % ns], (j / ns) & 1, p.watch);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t id = idesc_i8(128, p.Mt);
-      int slot = 0;
-      uint32_t ph = 0;
-      for (int i = 0; i < n; ++i) {
-        if (!mbar_wait(&full[slot], ph, p.watch, kErrTimeoutMma)) break;
-        tc_fence_after();
-        const uint32_t base = smem_u32(ring + slot * sb);
-        const uint64_t dw = sdesc_kmajor_sw128(base);
-        const uint64_t dx = sdesc_kmajor_sw128(base + 16384);
+    const uint32_t one = elect_one();
+    const uint32_t id = idesc_i8(128, p.Mt);
+    const uint64_t dw0 = sdesc_kmajor_sw128(smem_u32(ring)), dx0 = sdesc_kmajor_sw128(smem_u32(ring) + 16384);
+    int slot = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < n; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], ph, p.watch, kErrTimeoutMma))) break;
+      tc_fence_after();
+      const uint64_t dw = dw0 + static_cast<uint64_t>(slot * (sb >> 4)), dx = dx0 + static_cast<uint64_t>(slot * (sb >> 4));
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_i8(tbase, dw + 2 * kk, dx + 2 * kk, id, (i | kk) != 0 ? 1u : 0u);
-        tc_commit(&empty[slot]);
-        if (++slot == ns) { slot = 0; ph ^= 1; }
-        if (i + 1 == n) tc_commit(acc_full);
-      }
-      tc_commit(drain);
-      mbar_wait_drain(drain, 0, p.watch);
+      for (int kk = 0; kk < 4; ++kk) mma_i8(tbase, dw + 2 * kk, dx + 2 * kk, id, (i | kk) != 0 ? 1u : 0u, one);
+      commit_one(&empty[slot], one);
+      if (i + 1 == n) commit_one(acc_full, one);
+      if (++slot == ns) { slot = 0; ph ^= 1; }
     }
+    commit_one(drain, one);
+    if (one) mbar_wait_drain(drain, 0, p.watch);
+    __syncwarp();
   } else {
-    // The sums as [token][feature] in the ring, which is idle once the last
-    // MMA is done: a warp's lanes are 32 features of one token.
-    const int q = warp & 3;
+    // TMEM lane = feature, column = token; two warps share a lane quadrant and
+    // take alternate blocks of 16 tokens.
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int f = f0 + 32 * q + lane;
+    const float4 s2 = f < p.N ? __ldg(p.sb + f / 2) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float s = f & 1 ? s2.y : s2.x, b = f & 1 ? s2.w : s2.z;
     int* part = reinterpret_cast<int*>(ring) + 32 * q + lane;
     if (__all_sync(0xffffffffu, mbar_wait(acc_full, 0, p.watch, kErrTimeoutEpilogue))) {
       tc_fence_after();
-      for (int c = 0; c < p.Mt; c += 16) {
+      for (int c = 16 * half; c < p.Mt; c += 32) {
         uint32_t v[16];
         tmem_ld16_wait(tbase + ((32u * q) << 16) + c, v);
+        if (p.splits > 1) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) part[(c + i) * 128] = static_cast<int>(v[i]);
+          for (int i = 0; i < 16; ++i) part[(c + i) * 128] = static_cast<int>(v[i]);
+        } else {
+          i8_store_tokens<kAct>(v, c, p.M, p.N, f, s, b, p.sx, p.y);
+        }
       }
     } else {
       ok = false;
@@ -467,31 +602,50 @@ __global__ void __launch_bounds__(kIsThreads, 1) ll_i8_stream_kernel(const __gri
     tc_fence_after();
     tmem_dealloc(tbase, p.tmem_cols);
   }
+  if (p.splits == 1) return;
   // After a timeout the sums are incomplete; the CTA still takes part in both
   // cluster barriers.
-  if (p.splits > 1) cluster_sync();
-  const uint32_t part = smem_u32(ring);
-  for (int i = threadIdx.x; ok && i < ((p.M - z + p.splits - 1) / p.splits) * 64; i += kIsThreads) {
-    const int m = z + (i >> 6) * p.splits, c = (i & 63) * 2;
-    if (f0 + c >= p.N) continue;
-    const uint32_t off = part + static_cast<uint32_t>((m * 128 + c) * 4);
-    int2 acc = make_int2(0, 0);
-    if (p.splits == 1) {
-      acc = *reinterpret_cast<const int2*>(ring + (m * 128 + c) * 4);
-    } else {
+  cluster_sync();
+  const int c = 4 * lane;  // a warp's lanes are a token's 128 features
+  if (ok && f0 + c < p.N) {
+    const float4 s0v = __ldg(p.sb + (f0 + c) / 2), s1v = __ldg(p.sb + (f0 + c) / 2 + 1);
+    const uint32_t part = smem_u32(ring) + 4 * c;
+    for (int m = z + warp * p.splits; m < p.M; m += (kIsThreads / 32) * p.splits) {
+      const float sm = __ldg(p.sx + m);
+      int4 v[kIsMaxSplit];
 #pragma unroll
       for (int r = 0; r < kIsMaxSplit; ++r)
+        if (r < p.splits) v[r] = ld_shared_cluster_i4(mapa_shared(part + 512u * m, static_cast<uint32_t>(r)));
+      int4 a = v[0];
+#pragma unroll
+      for (int r = 1; r < kIsMaxSplit; ++r)
         if (r < p.splits) {
-          const int2 v = ld_shared_cluster_i2(mapa_shared(off, static_cast<uint32_t>(r)));
-          acc.x += v.x;
-          acc.y += v.y;
+          a.x += v[r].x;
+          a.y += v[r].y;
+          a.z += v[r].z;
+          a.w += v[r].w;
         }
+      *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(m) * p.N + f0 + c) =
+          make_uint2(i8_out2<kAct>(a.x, a.y, sm, s0v), i8_out2<kAct>(a.z, a.w, sm, s1v));
     }
-    *reinterpret_cast<uint32_t*>(p.y + static_cast<size_t>(m) * p.N + f0 + c) =
-        i8_out2<kAct>(acc.x, acc.y, __ldg(p.sx + m), __ldg(p.sb + (f0 + c) / 2));
   }
   __syncwarp();
-  if (p.splits > 1) cluster_sync();  // no CTA leaves while a peer still reads its sums
+  cluster_sync();  // no CTA leaves while a peer still reads its sums
+}
+
+// The weight as the kernels read it: panels of 128 codes of every row,
+// [K / 128][N][128], so that a tile's load of one K step is one contiguous
+// piece of memory; zeros behind K.
+__global__ void ll_i8_panels_kernel(const int8_t* __restrict__ w, int8_t* __restrict__ panels, int N, int K) {
+  const int nc = (K + 127) / 128 * 8;  // 16-byte chunks of a padded row
+  const size_t total = static_cast<size_t>(N) * nc;
+  for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < total;
+       i += static_cast<size_t>(gridDim.x) * blockDim.x) {
+    const int c = static_cast<int>(i % nc);
+    const size_t n = i / nc;
+    const uint4 v = 16 * c < K ? *reinterpret_cast<const uint4*>(w + n * K + 16 * c) : make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(panels + (static_cast<size_t>(c / 8) * N + n) * 128 + 16 * (c % 8)) = v;
+  }
 }
 
 // (scale, scale, bias, bias) of two features as the epilogues read them, zeros

@@ -14,7 +14,7 @@
 struct ll_i8_layer {
   int N = 0, K = 0, device = 0, num_sms = 0;
   bool ready = false;
-  int8_t* W = nullptr;   // [N, K]
+  int8_t* W = nullptr;   // panels [K / 128][N][128]
   float4* sb = nullptr;  // [N_pad / 2] (scale, scale, bias, bias), zeros behind the last feature
   int N_pad = 0;         // room for a tile of 256 features that starts at the last one
   int* status = nullptr;
@@ -85,8 +85,10 @@ int launch_rows_i8(const llk::RowsParams& p, bool norm, int sms, cudaStream_t st
 
 using I8Fn = void (*)(llk::I8Params);
 using I8StreamFn = void (*)(llk::I8StreamParams);
-I8Fn kernel_i8(int epilogue) {
-  return epilogue == LL_EPILOGUE_GELU_TANH ? llk::ll_i8_kernel<llk::kActGelu> : llk::ll_i8_kernel<llk::kActNone>;
+I8Fn kernel_i8(int epilogue, bool swap) {
+  using namespace llk;
+  if (epilogue == LL_EPILOGUE_GELU_TANH) return swap ? ll_i8_kernel<kActGelu, true> : ll_i8_kernel<kActGelu, false>;
+  return swap ? ll_i8_kernel<kActNone, true> : ll_i8_kernel<kActNone, false>;
 }
 I8StreamFn kernel_i8_stream(int epilogue) {
   return epilogue == LL_EPILOGUE_GELU_TANH ? llk::ll_i8_stream_kernel<llk::kActGelu>
@@ -98,8 +100,9 @@ I8StreamFn kernel_i8_stream(int epilogue) {
 bool setup_i8(ll_i8_layer* h) {
   using namespace llk;
   for (int e : {LL_EPILOGUE_NONE, LL_EPILOGUE_GELU_TANH})
-    if (cudaFuncSetAttribute(kernel_i8(e), cudaFuncAttributeMaxDynamicSharedMemorySize, i8_smem_bytes()) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel_i8_stream(e), cudaFuncAttributeMaxDynamicSharedMemorySize, kIsRing + 1280) !=
+    if (cudaFuncSetAttribute(kernel_i8(e, false), cudaFuncAttributeMaxDynamicSharedMemorySize, i8_smem_bytes()) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel_i8(e, true), cudaFuncAttributeMaxDynamicSharedMemorySize, i8_smem_bytes()) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel_i8_stream(e), cudaFuncAttributeMaxDynamicSharedMemorySize, kIsRingLarge + 1280) !=
             cudaSuccess)
       return false;
   for (int s = 2; s <= kIsMaxSplit; ++s) {
@@ -111,7 +114,7 @@ bool setup_i8(ll_i8_layer* h) {
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(h->num_sms, s);
     cfg.blockDim = dim3(kIsThreads);
-    cfg.dynamicSmemBytes = kIsRing + 1280;
+    cfg.dynamicSmemBytes = kIsRingLarge + 1280;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&h->clusters[s], kernel_i8_stream(LL_EPILOGUE_NONE), &cfg) != cudaSuccess)
@@ -121,15 +124,81 @@ bool setup_i8(ll_i8_layer* h) {
   return true;
 }
 
-constexpr int kI8StreamMaxM = 256;
+bool make_weight_map(const ll_i8_layer* h, CUtensorMap* m, int rows) {
+  return make_map3(m, h->W, CU_TENSOR_MAP_DATA_TYPE_UINT8, 128, h->N, (h->K + 127) / 128, 128,
+                   128ull * h->N, 128, static_cast<uint32_t>(rows), 1, CU_TENSOR_MAP_SWIZZLE_128B);
+}
 
-int launch_i8_stream(const ll_i8_layer* h, const void* codes, const float* scale, void* y, int M, cudaStream_t st) {
+constexpr int kI8StreamMaxM = 256;  // the MMA's N
+
+// What a forward of M tokens runs, and the model's cycles.  The model's rates
+// are fitted to measured times (at about 1.75 GHz); it ranks plans and is not a
+// prediction of the time:
+//   a CTA's loads arrive at 66 bytes a cycle (w = 64, 128 and 256 of the pair
+//   kernel: 310, 367 and 565 cycles per K step), the weight at 5.7 TB/s;
+//   products of a 256 x w step take 2.2 w cycles (2 w alone);
+//   start and end cost 5,000 (pair) or 5,560 (streaming), and the last tile's
+//   epilogue 4,500 per 256 columns (11,000 with kSwap's stores token by token)
+//   or 42 per token (streaming).
+struct I8Plan {
+  bool stream;
+  int splits, steps;  // streaming: CTAs per tile and K steps of each
+  bool swap;          // pairs: orientation, tiles of a and b, and b's width
+  int na, nb, w;
+  double cycles;
+};
+
+double i8_weight_cycles(const ll_i8_layer* h) { return static_cast<double>(h->N) * h->K * 3.07e-4; }
+
+I8Plan i8_plan_pair(const ll_i8_layer* h, int M) {
+  const int pairs = h->num_sms / 2;
+  const double steps = (h->K + 127) / 128;
+  I8Plan best{};
+  best.cycles = -1;
+  for (bool swap : {false, true}) {
+    const int na = ((swap ? h->N : M) + 255) / 256, b = swap ? M : h->N;
+    for (int w = 256; w >= 64; w -= 32) {
+      const int nb = (b + w - 1) / w;
+      const double waves = std::ceil(static_cast<double>(na) * nb / pairs);
+      const double loop = waves * (steps * std::max(2.2 * w, (16384.0 + 64.0 * w) / 66.0) + 200.0);
+      const double cycles = 5000.0 + std::max(loop, i8_weight_cycles(h)) + (swap ? 11000.0 : 4500.0) * w / 256;
+      if (best.cycles < 0 || cycles < 0.98 * best.cycles) best = I8Plan{false, 0, 0, swap, na, nb, w, cycles};
+    }
+  }
+  return best;
+}
+
+I8Plan i8_plan_stream(const ll_i8_layer* h, int M) {
+  const int tiles = (h->N + 127) / 128, steps = (h->K + 127) / 128, Mt = (M + 15) / 16 * 16;
+  // As many CTAs as fit at once share the K steps of a tile.
+  int s = 1;
+  while (s < std::min(llk::kIsMaxSplit, steps) && tiles <= h->clusters[s + 1]) ++s;
+  I8Plan p{};
+  p.stream = true;
+  p.steps = (steps + s - 1) / s;
+  p.splits = (steps + p.steps - 1) / p.steps;
+  const double waves = std::ceil(static_cast<double>(tiles) * p.splits / h->num_sms);
+  p.cycles = 5560.0 + std::max(waves * p.steps * (16384.0 + 128.0 * Mt) / 66.0, i8_weight_cycles(h)) + 42.0 * M;
+  return p;
+}
+
+// Measured (us, streaming / pair): 1024 -> 1024: M = 32 4.1 / 4.6, 128 6.0 /
+// 4.7; 4096 -> 4096: 64 7.0 / 9.8, 256 11.3 / 10.2; 4096 -> 16384: 64 14.3 /
+// 14.9, 256 24.5 / 18.4; 8192 -> 2048: 256 12.8 / 14.6.
+I8Plan i8_plan(const ll_i8_layer* h, int M) {
+  const I8Plan pair = i8_plan_pair(h, M);
+  if (M > kI8StreamMaxM) return pair;
+  const I8Plan stream = i8_plan_stream(h, M);
+  return pair.cycles < 0.95 * stream.cycles ? pair : stream;
+}
+
+int launch_i8_stream(const ll_i8_layer* h, const I8Plan& plan, const void* codes, const float* scale, void* y, int M,
+                     cudaStream_t st) {
   using namespace llk;
-  constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   I8StreamParams p;
   p.Mt = (M + 15) / 16 * 16;
-  if (!make_map(&p.tm_x, codes, kU8, M, h->K, h->K, 128, p.Mt, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map(&p.tm_w, h->W, kU8, h->N, h->K, h->K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+  if (!make_map(&p.tm_x, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, M, h->K, h->K, 128, p.Mt, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_weight_map(h, &p.tm_w, 128))
     return LL_ERR_CUDA;
   p.sx = scale;
   p.sb = h->sb;
@@ -140,11 +209,13 @@ int launch_i8_stream(const ll_i8_layer* h, const void* codes, const float* scale
   p.tmem_cols = next_pow2_ge32(p.Mt);
   p.withhold = h->withhold;
   p.watch = Watch{h->status, h->timeout_ns};
-  const int tiles = (h->N + 127) / 128, steps = (h->K + 127) / 128;
-  int s = 1;
-  while (s < std::min(kIsMaxSplit, steps) && tiles <= h->clusters[s + 1]) ++s;
-  p.steps = (steps + s - 1) / s;
-  p.splits = (steps + p.steps - 1) / p.steps;
+  p.steps = plan.steps;
+  p.splits = plan.splits;
+  // At least four slots: a split's sums (512 bytes per token) go where the ring
+  // was, and 4 (16384 + 128 Mt) >= 512 Mt.
+  const bool small = is_stages(p.Mt, kIsRingSmall) >= 4 && (p.Mt <= 32 || p.steps <= 16);
+  const int ring = small ? kIsRingSmall : kIsRingLarge;
+  p.stages = is_stages(p.Mt, ring);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -153,44 +224,47 @@ int launch_i8_stream(const ll_i8_layer* h, const void* codes, const float* scale
   attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = static_cast<unsigned>(p.splits);
   attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(tiles, p.splits);
+  cfg.gridDim = dim3((h->N + 127) / 128, p.splits);
   cfg.blockDim = dim3(kIsThreads);
-  cfg.dynamicSmemBytes = is_smem_bytes(p.Mt);
+  cfg.dynamicSmemBytes = is_smem_bytes(p.Mt, ring);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = p.splits > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel_i8_stream(h->epilogue), p) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
 }
 
-int launch_i8(const ll_i8_layer* h, const void* codes, const float* scale, void* y, int M, cudaStream_t st) {
+int launch_i8(const ll_i8_layer* h, const I8Plan& plan, const void* codes, const float* scale, void* y, int M,
+              cudaStream_t st) {
   using namespace llk;
-  constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   I8Params p;
-  p.fn = 256;
-  if (!make_map(&p.tm_x, codes, kU8, M, h->K, h->K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map(&p.tm_w, h->W, kU8, h->N, h->K, h->K, 128, p.fn / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  p.na = plan.na;
+  p.nb = plan.nb;
+  p.w = plan.w;
+  if (!make_map(&p.tm_x, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, M, h->K, h->K, 128, plan.swap ? p.w / 2 : 128,
+                CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_weight_map(h, &p.tm_w, plan.swap ? 128 : p.w / 2) ||
       !make_map(&p.tm_y, y, kBF16, M, h->N, 2ull * h->N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return LL_ERR_CUDA;
   p.sx = scale;
   p.sb = h->sb;
+  p.y = static_cast<uint16_t*>(y);
   p.M = M;
   p.N = h->N;
   p.K = h->K;
-  p.n_ttiles = (M + 255) / 256;
-  p.n_ftiles = (h->N + p.fn - 1) / p.fn;
   p.withhold = h->withhold;
   p.watch = Watch{h->status, h->timeout_ns};
+  const long long tiles = static_cast<long long>(p.na) * p.nb;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(2 * std::min(p.n_ttiles * p.n_ftiles, h->num_sms / 2));
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long long>(tiles, h->num_sms / 2)));
   cfg.blockDim = dim3(kI8Threads);
   cfg.dynamicSmemBytes = i8_smem_bytes();
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel_i8(h->epilogue), p) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel_i8(h->epilogue, plan.swap), p) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
 }
 
 void free_i8(ll_i8_layer* h) {
@@ -295,7 +369,7 @@ ll_i8_handle ll_i8_create(int N, int K) {
   h->device = dev;
   h->num_sms = sms;
   h->N_pad = (N + 511) / 256 * 256;
-  if (cudaMalloc(&h->W, static_cast<size_t>(N) * K) != cudaSuccess ||
+  if (cudaMalloc(&h->W, static_cast<size_t>(N) * ((K + 127) / 128 * 128)) != cudaSuccess ||
       cudaMalloc(&h->sb, sizeof(float4) * (h->N_pad / 2)) != cudaSuccess || cudaMalloc(&h->status, sizeof(int)) != cudaSuccess) {
     cudaGetLastError();
     free_i8(h);
@@ -336,10 +410,10 @@ int ll_i8_set_weights(ll_i8_handle h, const void* codes, const float* scale, con
   if (ok && !finite) return fail(LL_ERR_INVALID_ARG);
   if (ok) {
     h->ready = false;
-    ok = cudaMemcpy(h->W, codes, static_cast<size_t>(h->N) * h->K, cudaMemcpyDeviceToDevice) == cudaSuccess;
+    llk::ll_i8_panels_kernel<<<h->num_sms * 8, 256>>>(static_cast<const int8_t*>(codes), h->W, h->N, h->K);
     llk::ll_i8_scale_bias_kernel<<<(h->N_pad / 2 + 255) / 256, 256>>>(scale, static_cast<const uint16_t*>(bias), h->sb, h->N,
                                                                  h->N_pad);
-    ok = ok && cudaGetLastError() == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
+    ok = cudaGetLastError() == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
   }
   if (!ok) {
     cudaGetLastError();
@@ -375,7 +449,8 @@ int ll_i8_forward(ll_i8_handle h, const void* codes, const float* scale, void* y
   if (dev != h->device || !is_device_ptr_on(codes, dev) || !is_device_ptr_on(scale, dev) || !is_device_ptr_on(y, dev))
     return fail(LL_ERR_INVALID_ARG);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int rc = M <= kI8StreamMaxM ? launch_i8_stream(h, codes, scale, y, M, st) : launch_i8(h, codes, scale, y, M, st);
+  const I8Plan plan = i8_plan(h, M);
+  const int rc = plan.stream ? launch_i8_stream(h, plan, codes, scale, y, M, st) : launch_i8(h, plan, codes, scale, y, M, st);
   if (rc != LL_OK) cudaGetLastError();
   return rc == LL_OK ? LL_OK : fail(rc);
 }
