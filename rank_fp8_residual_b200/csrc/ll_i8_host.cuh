@@ -47,12 +47,16 @@ struct DeviceScope {
 };
 
 template <bool kNorm>
-cudaError_t launch_rows_i8_as(const llk::RowsParams& p, int chunks, const cudaLaunchConfig_t& cfg) {
+cudaError_t launch_rows_i8_as(const llk::RowsParams& p, int chunks, bool keep, const cudaLaunchConfig_t& cfg) {
+  using namespace llk;
   switch (chunks) {
-    case 1: return cudaLaunchKernelEx(&cfg, llk::ll_rows_i8_kernel<1, kNorm>, p);
-    case 2: return cudaLaunchKernelEx(&cfg, llk::ll_rows_i8_kernel<2, kNorm>, p);
-    case 4: return cudaLaunchKernelEx(&cfg, llk::ll_rows_i8_kernel<4, kNorm>, p);
-    default: return cudaLaunchKernelEx(&cfg, llk::ll_rows_i8_kernel<8, kNorm>, p);
+    case 1: return cudaLaunchKernelEx(&cfg, ll_rows_i8_kernel<1, kNorm, true>, p);
+    case 2: return cudaLaunchKernelEx(&cfg, ll_rows_i8_kernel<2, kNorm, true>, p);
+    case 4:
+      if constexpr (kNorm)
+        if (keep) return cudaLaunchKernelEx(&cfg, ll_rows_i8_kernel<4, true, true>, p);
+      return cudaLaunchKernelEx(&cfg, ll_rows_i8_kernel<4, kNorm, false>, p);
+    default: return cudaLaunchKernelEx(&cfg, ll_rows_i8_kernel<8, kNorm, false>, p);
   }
 }
 
@@ -62,9 +66,9 @@ int launch_rows_i8(const llk::RowsParams& p, bool norm, int sms, cudaStream_t st
   // are (latency).  Many: four chunks, whose loads are in flight together.
   // Norm with residual, us with 1 / 2 / 4 chunks: 100 x 8192 2.8 / 3.2 / 3.2,
   // 400 x 4096 5.0 / 3.9 / 4.2, 3630 x 4096 29.2 / 19.9 / 18.0, 16384 x 4096
-  // 118 / 78 / 69.  Eight where four would need more than 256 threads.
+  // 118 / 78 / 69.  Eight where four would need more than 1024 threads.
   int c = p.M <= 2 * sms ? 1 : (p.M <= 8 * sms && nv <= 512 ? 2 : 4);
-  while (c < 8 && nv > llk::rows_max_threads(c) * c) c *= 2;
+  while (c < 8 && nv > 1024 * c) c *= 2;
   while (c > 1 && nv <= 16 * c) c /= 2;
   const int threads = ((nv + c - 1) / c + 31) / 32 * 32;
   // Rows of one warp: four per block (16384 x 512 11.1 us, one per block 19.9).
@@ -78,7 +82,7 @@ int launch_rows_i8(const llk::RowsParams& p, bool norm, int sms, cudaStream_t st
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((norm ? launch_rows_i8_as<true>(p, c, cfg) : launch_rows_i8_as<false>(p, c, cfg)) == cudaSuccess) return LL_OK;
+  if ((norm ? launch_rows_i8_as<true>(p, c, threads <= 256, cfg) : launch_rows_i8_as<false>(p, c, false, cfg)) == cudaSuccess) return LL_OK;
   cudaGetLastError();
   return LL_ERR_CUDA;
 }

@@ -46,31 +46,15 @@ struct RowsParams {
 
 constexpr float kRound = 12582912.f;  // 1.5 * 2^23
 constexpr int kRowsMaxK = 1024 * 8 * 8;  // 1024 threads with 8 chunks of 8 values each
-// Threads per row that a kernel with c chunks per thread may have.
-constexpr int rows_max_threads(int c) { return c == 4 ? 256 : 1024; }
+// Threads per row that a kernel may have: 1024, or 256 for four chunks per
+// thread with u kept.
+constexpr int rows_max_threads(int c, bool keep) { return c == 4 && keep ? 256 : 1024; }
 
-// Products of the low and the high bf16 of two words in binary32 (exact: 16
-// bits), added to c.  The mixed-precision fused multiply-add takes the bf16
-// halves as they are, on the multiply-add pipe; unpacking them first costs an
-// operation each on the pipe that already bounds these kernels.
-__device__ __forceinline__ float fma_lo(uint32_t a, uint32_t b, float c) {
-  float d;
-  asm("{\n\t.reg .b16 al, ah, bl, bh;\n\tmov.b32 {al, ah}, %1;\n\tmov.b32 {bl, bh}, %2;\n\t"
-      "fma.rn.f32.bf16 %0, al, bl, %3;\n\t}"
-      : "=f"(d)
-      : "r"(a), "r"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float fma_hi(uint32_t a, uint32_t b, float c) {
-  float d;
-  asm("{\n\t.reg .b16 al, ah, bl, bh;\n\tmov.b32 {al, ah}, %1;\n\tmov.b32 {bl, bh}, %2;\n\t"
-      "fma.rn.f32.bf16 %0, ah, bh, %3;\n\t}"
-      : "=f"(d)
-      : "r"(a), "r"(b), "f"(c));
-  return d;
+// The two bf16 of a word.
+__device__ __forceinline__ float2 bf16x2_to_f32x2(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
 constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones
-constexpr uint32_t k127s = 0x42FE42FEu;  // two bf16 127s
 // Two maxima of magnitudes, NaN where either is.
 __device__ __forceinline__ uint32_t absmax2_nan(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -84,33 +68,35 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// max(a, |b|), NaN if either is.
-__device__ __forceinline__ float absmax_nan(float a, float b) {
+// max(a, |b.x|, |b.y|) for a >= 0, NaN if any is.
+__device__ __forceinline__ float absmax_nan(float a, float2 b) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b.x), "f"(b.y));
   return r;
 }
 
-// The code of p / a in the low byte, p = 127 u (see above).
-__device__ __forceinline__ uint32_t code_of(float p, float a, float y) {
-  const float q0 = p * y;
-  return __float_as_uint(fmaf(fmaf(-q0, a, p), y, q0) + kRound);
+// The codes of p / a in the low bytes, p = 127 u (see above); na = -a, y ~ 1 / a.
+__device__ __forceinline__ float2 codes_of(float2 p, float2 na, float2 y) {
+  const float2 q0 = mul2(p, y);
+  return add2(fma2(fma2(q0, na, p), y, q0), make_float2(kRound, kRound));
 }
-__device__ __forceinline__ uint32_t pack_codes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+__device__ __forceinline__ uint32_t pack_codes(float2 a, float2 b) {
+  return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                     __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
 
 // One row per blockIdx.x and threadIdx.y: kC chunks of eight values for each
 // of blockDim.x threads (a multiple of 32; one warp where blockDim.y > 1).
 // kNorm: the norm, else the quantisation alone.
 //
-// A norm's u stays in registers between the maximum and the codes up to four
-// chunks per thread; with eight it would spill, so there h stays (packed) and
-// the products are taken once more.
-template <int kC, bool kNorm>
-__global__ void __launch_bounds__(rows_max_threads(kC)) ll_rows_i8_kernel(const RowsParams p) {
-  __shared__ float s_sum[2][32];
-  __shared__ uint32_t s_max[32];
+// kKeep: a norm's u stays in registers between the maximum and the codes (up
+// to four chunks and 256 threads; beyond, that would cost the second block on
+// an SM, so h stays, packed, and the products are taken once more: 4096 x
+// 16384 with residual 71 us, 90 with u kept).
+template <int kC, bool kNorm, bool kKeep>
+__global__ void __launch_bounds__(rows_max_threads(kC, kKeep)) ll_rows_i8_kernel(const RowsParams p) {
+  __shared__ __align__(16) float s_sum[2][32];
+  __shared__ __align__(16) uint32_t s_max[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nw = blockDim.x >> 5;
   const int nv = p.K >> 3;
@@ -128,14 +114,20 @@ __global__ void __launch_bounds__(rows_max_threads(kC)) ll_rows_i8_kernel(const 
       rv[j] = c < nv ? reinterpret_cast<const uint4*>(p.residual + row)[c] : make_uint4(0, 0, 0, 0);
   }
   const auto gain = [&](int c) {
-    return p.w && c < nv ? __ldg(reinterpret_cast<const uint4*>(p.w) + c) : make_uint4(kOnes, kOnes, kOnes, kOnes);
+    return c < nv ? __ldg(reinterpret_cast<const uint4*>(p.w) + c) : make_uint4(kOnes, kOnes, kOnes, kOnes);
   };
-  constexpr bool kKeep = kC <= 4;
-  float u[kKeep ? kC : 1][8];  // of the norm
+  constexpr bool kAhead = kC <= 4;  // the gains' loads go out with x's
+  uint4 wv[kAhead ? kC : 1];
+  if (kNorm && kAhead && p.w) {
+#pragma unroll
+    for (int j = 0; j < kC; ++j) wv[kAhead ? j : 0] = gain(threadIdx.x + j * blockDim.x);
+  }
+  float2 u[kKeep ? kC : 1][4];  // of the norm
   float ss = 0.f;
   uint32_t mx = 0;  // max |u| as bits: NaN above infinity above every finite value
   if (kNorm) {
     float am = 0.f;
+    float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
       const int c = threadIdx.x + j * blockDim.x;
@@ -146,20 +138,26 @@ __global__ void __launch_bounds__(rows_max_threads(kC)) ll_rows_i8_kernel(const 
         hv[j].w = add_bf16x2(hv[j].w, rv[j].w);
         if (p.h && c < nv) reinterpret_cast<uint4*>(p.h + row)[c] = hv[j];
       }
-      const uint4 wv = gain(c);
-      const uint32_t hw[4] = {hv[j].x, hv[j].y, hv[j].z, hv[j].w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
+      const uint32_t hw[4] = {hv[j].x, hv[j].y, hv[j].z, hv[j].w};
+      float2 uj[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        ss = fma_lo(hw[i], hw[i], ss);
-        ss = fma_hi(hw[i], hw[i], ss);
-        const float u0 = fma_lo(hw[i], ww[i], 0.f), u1 = fma_hi(hw[i], ww[i], 0.f);
-        am = absmax_nan(absmax_nan(am, u0), u1);
-        if (kKeep) {
-          u[j][2 * i] = u0;
-          u[j][2 * i + 1] = u1;
-        }
+        uj[i] = bf16x2_to_f32x2(hw[i]);
+        s2 = fma2(uj[i], uj[i], s2);
+      }
+      if (p.w) {
+        const uint4 wj = kAhead ? wv[kAhead ? j : 0] : gain(c);
+        const uint32_t ww[4] = {wj.x, wj.y, wj.z, wj.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) uj[i] = mul2(uj[i], bf16x2_to_f32x2(ww[i]));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        am = absmax_nan(am, uj[i]);
+        if (kKeep) u[j][i] = uj[i];
       }
     }
+    ss = s2.x + s2.y;
     mx = __float_as_uint(am);
   } else {
     uint32_t m2 = 0;  // two bf16 magnitudes (positive: the order of the bits is that of the values)
@@ -185,8 +183,23 @@ __global__ void __launch_bounds__(rows_max_threads(kC)) ll_rows_i8_kernel(const 
       s_sum[0][warp] = ss;
     }
     __syncthreads();
-    mx = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[lane] : 0u);
-    if (kNorm) ss = warp_sum(lane < nw ? s_sum[0][lane] : 0.f);
+    if (nw <= 4) {
+      const uint4 m4 = *reinterpret_cast<const uint4*>(s_max);
+      const float4 t4 = *reinterpret_cast<const float4*>(s_sum[0]);
+      mx = max(m4.x, m4.y);
+      ss = t4.x + t4.y;
+      if (nw > 2) {
+        mx = max(mx, m4.z);
+        ss += t4.z;
+      }
+      if (nw > 3) {
+        mx = max(mx, m4.w);
+        ss += t4.w;
+      }
+    } else {
+      mx = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[lane] : 0u);
+      if (kNorm) ss = warp_sum(lane < nw ? s_sum[0][lane] : 0.f);
+    }
   }
   float a = __uint_as_float(mx), rstd = 1.f;
   const bool bad = mx >= 0x7F800000u;
@@ -206,9 +219,9 @@ __global__ void __launch_bounds__(rows_max_threads(kC)) ll_rows_i8_kernel(const 
         const uint32_t hw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float h0 = fma_lo(hw[i], kOnes, 0.f) * 0x1p-64f, h1 = fma_hi(hw[i], kOnes, 0.f) * 0x1p-64f;
-          s2 = fmaf(h0, h0, s2);
-          s2 = fmaf(h1, h1, s2);
+          const float2 t = bf16x2_to_f32x2(hw[i]);
+          s2 = fmaf(t.x * 0x1p-64f, t.x * 0x1p-64f, s2);
+          s2 = fmaf(t.y * 0x1p-64f, t.y * 0x1p-64f, s2);
         }
       }
       s2 = warp_sum(s2);
@@ -227,51 +240,45 @@ __global__ void __launch_bounds__(rows_max_threads(kC)) ll_rows_i8_kernel(const 
   const float pre = a > 0x1p100f ? 0x1p-60f : (a < 0x1p-60f ? 0x1p80f : 1.f);
   const float pre127 = 127.f * pre;
   a *= pre;
-  const float yr = a > 0.f ? __frcp_rn(a) : 0.f;
+  const float yr = a > 0.f ? __fdividef(1.f, a) : 0.f;
+  const float2 y2 = make_float2(yr, yr), na2 = make_float2(-a, -a), p127 = make_float2(pre127, pre127);
+  const float2 r2 = make_float2(rstd, rstd);
 #pragma unroll
   for (int j = 0; j < kC; ++j) {
     const int c = threadIdx.x + j * blockDim.x;
     if (c >= nv) break;
-    float v[8];  // 127 u
-    if (kNorm) {
-      float(&uj)[8] = u[kKeep ? j : 0];
-      if (!kKeep) {
-        const uint4 wv = gain(c);
-        const uint32_t hw[4] = {hv[j].x, hv[j].y, hv[j].z, hv[j].w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
+    float2 v[4];
+    if (kNorm && kKeep) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uj[2 * i] = fma_lo(hw[i], ww[i], 0.f);
-          uj[2 * i + 1] = fma_hi(hw[i], ww[i], 0.f);
-        }
-      }
-      if (p.y)
-        reinterpret_cast<uint4*>(p.y + row)[c] =
-            make_uint4(pack_bf16x2(uj[0] * rstd, uj[1] * rstd), pack_bf16x2(uj[2] * rstd, uj[3] * rstd),
-                       pack_bf16x2(uj[4] * rstd, uj[5] * rstd), pack_bf16x2(uj[6] * rstd, uj[7] * rstd));
-      if (!p.codes) continue;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = uj[i] * pre127;
+      for (int i = 0; i < 4; ++i) v[i] = u[j][i];
     } else {
       const uint32_t hw[4] = {hv[j].x, hv[j].y, hv[j].z, hv[j].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = fma_lo(hw[i], k127s, 0.f);
-        v[2 * i + 1] = fma_hi(hw[i], k127s, 0.f);
+      for (int i = 0; i < 4; ++i) v[i] = bf16x2_to_f32x2(hw[i]);
+      if (kNorm && p.w) {
+        const uint4 wj = gain(c);
+        const uint32_t ww[4] = {wj.x, wj.y, wj.z, wj.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], bf16x2_to_f32x2(ww[i]));
       }
-      if (pre127 != 127.f) {
+    }
+    if (kNorm) {
+      if (p.y) {
+        uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          v[2 * i] = fma_lo(hw[i], kOnes, 0.f) * pre127;
-          v[2 * i + 1] = fma_hi(hw[i], kOnes, 0.f) * pre127;
+          const float2 t = mul2(v[i], r2);
+          o[i] = pack_bf16x2(t.x, t.y);
         }
+        reinterpret_cast<uint4*>(p.y + row)[c] = make_uint4(o[0], o[1], o[2], o[3]);
       }
+      if (!p.codes) continue;
     }
     uint2 out = make_uint2(0u, 0u);
     if (!bad) {
-      uint32_t r[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = code_of(v[i], a, yr);
-      out = make_uint2(pack_codes(r[0], r[1], r[2], r[3]), pack_codes(r[4], r[5], r[6], r[7]));
+      for (int i = 0; i < 4; ++i) v[i] = codes_of(mul2(v[i], p127), na2, y2);
+      out = make_uint2(pack_codes(v[0], v[1]), pack_codes(v[2], v[3]));
     }
     reinterpret_cast<uint2*>(p.codes + row)[c] = out;
   }
