@@ -154,6 +154,14 @@ __device__ __forceinline__ uint32_t i8_out2(int a0, int a1, float sm, const floa
   return pack_bf16x2(v.x, v.y);
 }
 
+// A read-only load that stays where it stands: ahead of a wait whose time covers
+// its latency.
+__device__ __forceinline__ float4 ldg_ahead(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
+
 // Outputs of one feature (this lane's; s, b its scale and bias) for the 16
 // tokens from m0 on: a warp's lanes are 32 neighbouring features, 64 bytes of
 // a token's row.
@@ -377,6 +385,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       } else if (row < p.M) {
         sm = __ldg(p.sx + row);
       }
+      float4 sb[16];  // of the next chunk's features
+      auto load_sb = [&](int c) {
+        const float4* sb4 = p.sb + (b0 + c) / 2;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sb[i] = ldg_ahead(sb4 + i);
+      };
+      if (!kSwap && 32 * half < w) load_sb(32 * half);
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], (it >> 1) & 1, p.watch, kErrTimeoutEpilogue))) break;
       tc_fence_after();
       const uint32_t acc = tl + 256u * buf;
@@ -391,11 +406,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
           const int f = b0 + c;
           uint32_t v[32];
           tmem_ld32_wait(acc + c, v);
-          const float4* sb4 = p.sb + f / 2;
           uint32_t o[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            o[i] = i8_out2<kAct>(static_cast<int>(v[2 * i]), static_cast<int>(v[2 * i + 1]), sm, __ldg(sb4 + i));
+            o[i] = i8_out2<kAct>(static_cast<int>(v[2 * i]), static_cast<int>(v[2 * i + 1]), sm, sb[i]);
+          if (c + 64 < w) load_sb(c + 64);
           if (lane == 0) tma_store_wait_read<1>();
           __syncwarp();
           uint8_t* st = stg + eb * (32 * 64);
