@@ -154,6 +154,16 @@ __device__ __forceinline__ uint32_t i8_out2(int a0, int a1, float sm, const floa
   return pack_bf16x2(v.x, v.y);
 }
 
+// The tile's store to y and its bulk group, by the lane for which `one` holds.
+__device__ __forceinline__ void store_2d_one(const CUtensorMap* m, uint32_t src, int c0, int c1, bool in, bool one) {
+  asm volatile(
+      "{\n\t.reg .pred e, f;\n\tsetp.ne.b32 e, %4, 0;\n\tsetp.ne.b32 f, %5, 0;\n\t"
+      "@e cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
+      "@f cp.async.bulk.commit_group;\n\t}" ::"l"(m),
+      "r"(src), "r"(c0), "r"(c1), "r"(static_cast<uint32_t>(in && one)), "r"(static_cast<uint32_t>(one))
+      : "memory");
+}
+
 // A read-only load that stays where it stands: ahead of a wait whose time covers
 // its latency.
 __device__ __forceinline__ float4 ldg_ahead(const float4* p) {
@@ -420,10 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
                 make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            if (row0 < p.M && f < p.N) tma_store_2d(&p.tm_y, st, f, row0);
-            tma_store_commit();
-          }
+          store_2d_one(&p.tm_y, smem_u32(st), f, row0, row0 < p.M && f < p.N, lane == 0);
           eb ^= 1;
         }
       }
