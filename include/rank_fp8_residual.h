@@ -432,6 +432,20 @@ int ll_i8_set_epilogue(ll_i8_handle h, int epilogue);
  * before ll_i8_set_weights. */
 int ll_i8_forward(ll_i8_handle h, const void *codes, const float *scale, void *y, int M, void *stream);
 
+/* What a forward of M tokens through an (N, K) int8 layer runs on a GPU with
+ * num_sms SMs; host arithmetic only, as ll_plan.
+ *   kernel:        LL_I8_STREAM (few tokens: 128 features x all tokens per
+ *                  tile, K split over the CTAs of a cluster), LL_I8_PAIR (CTA
+ *                  pairs, 256 tokens x tile_features) or LL_I8_PAIR_SWAP (256
+ *                  features x tile_tokens).
+ *   tile_features, tile_tokens: the tile's size.
+ *   splits:        CTAs per tile of LL_I8_STREAM (else 1).
+ * A forward asks the occupancy calculator how many clusters fit; this call
+ * takes num_sms / splits.  Any out-pointer may be NULL.  LL_ERR_INVALID_ARG
+ * and LL_ERR_UNSUPPORTED as ll_i8_create, and for M < 1 or num_sms < 2. */
+enum { LL_I8_STREAM = 0, LL_I8_PAIR = 1, LL_I8_PAIR_SWAP = 2 };
+int ll_i8_plan(int N, int K, int M, int num_sms, int *kernel, int *tile_features, int *tile_tokens, int *splits);
+
 /* As ll_status, ll_set_debug and ll_destroy, for an int8 layer. */
 int ll_i8_status(ll_i8_handle h);
 int ll_i8_set_debug(ll_i8_handle h, int withhold_producer, uint64_t timeout_ns);

@@ -39,6 +39,10 @@ LL_VARIANT_FP8_SPLIT = 5
 LL_VARIANT_FP8_ACT = 6
 LL_VARIANT_GEMV = 7
 
+LL_I8_STREAM = 0
+LL_I8_PAIR = 1
+LL_I8_PAIR_SWAP = 2
+
 LL_EPILOGUE_NONE = 0
 LL_EPILOGUE_GELU_TANH = 1
 LL_EPILOGUE_GEGLU_TANH = 2
@@ -75,6 +79,7 @@ _SIGNATURES = {
     "ll_i8_set_weights": (ctypes.c_int, [_P, _P, _P, _P]),
     "ll_i8_set_epilogue": (ctypes.c_int, [_P, ctypes.c_int]),
     "ll_i8_forward": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, _P]),
+    "ll_i8_plan": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P, _P, _P]),
     "ll_i8_status": (ctypes.c_int, [_P]),
     "ll_i8_set_debug": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_uint64]),
     "ll_i8_destroy": (None, [_P]),
@@ -347,6 +352,16 @@ def ll_i8_forward(h: int, codes, scale, y, M: int, stream=None) -> None:
     rc = _lib.ll_i8_forward(h, _addr(codes), _addr(scale), _addr(y), int(M), _stream(stream))
     if rc != LL_OK:
         raise LLError(rc, "ll_i8_forward")
+
+
+def ll_i8_plan(N: int, K: int, M: int, num_sms: int):
+    """(kernel, features per tile, tokens per tile, CTAs per tile) of a forward
+    of M tokens through an (N, K) int8 layer.  Host arithmetic only."""
+    out = [ctypes.c_int(0) for _ in range(4)]
+    rc = _lib.ll_i8_plan(int(N), int(K), int(M), int(num_sms), *(ctypes.byref(v) for v in out))
+    if rc != LL_OK:
+        raise LLError(rc, "ll_i8_plan")
+    return tuple(v.value for v in out)
 
 
 def ll_i8_status(h: int) -> int:

@@ -459,6 +459,23 @@ int ll_i8_forward(ll_i8_handle h, const void* codes, const float* scale, void* y
   return rc == LL_OK ? LL_OK : fail(rc);
 }
 
+int ll_i8_plan(int N, int K, int M, int num_sms, int* kernel, int* tile_features, int* tile_tokens, int* splits) {
+  g_last_error = LL_OK;
+  if (N < 1 || N % 8 != 0 || K < 16 || K % 16 != 0 || M < 1 || num_sms < 2) return fail(LL_ERR_INVALID_ARG);
+  if (K > llk::kI8MaxK) return fail(LL_ERR_UNSUPPORTED);
+  ll_i8_layer view;  // what the planning reads
+  view.N = N;
+  view.K = K;
+  view.num_sms = num_sms;
+  for (int s = 1; s <= llk::kIsMaxSplit; ++s) view.clusters[s] = num_sms / s;
+  const I8Plan p = i8_plan(&view, M);
+  if (kernel) *kernel = p.stream ? LL_I8_STREAM : p.swap ? LL_I8_PAIR_SWAP : LL_I8_PAIR;
+  if (tile_features) *tile_features = p.stream ? 128 : p.swap ? 256 : p.w;
+  if (tile_tokens) *tile_tokens = p.stream ? (M + 15) / 16 * 16 : p.swap ? p.w : 256;
+  if (splits) *splits = p.stream ? p.splits : 1;
+  return LL_OK;
+}
+
 int ll_i8_status(ll_i8_handle h) {
   g_last_error = LL_OK;
   if (!h) return fail(LL_ERR_INVALID_ARG);

@@ -243,7 +243,11 @@ PRODUCT_SHAPES = [(1, 16, 8), (1, 4096, 1000), (2, 64, 136), (3, 2048, 2048), (4
                   (48, 640, 1032), (64, 4096, 2048), (65, 2000, 136), (100, 1040, 1000), (127, 256, 264),
                   (128, 2048, 512), (129, 2064, 128), (200, 4096, 1024), (255, 80, 256), (256, 1024, 2048),
                   (257, 272, 504), (333, 1040, 1000), (384, 4096, 768), (511, 128, 2056), (512, 2048, 2048),
-                  (700, 336, 120), (1025, 512, 1536), (1300, 2048, 2048), (2500, 144, 4096)]
+                  (700, 336, 120), (1025, 512, 1536), (1300, 2048, 2048), (2500, 144, 4096),
+                  # features on the pairs' long side, tokens in narrow tiles
+                  (65, 2064, 16384), (96, 4096, 16392), (128, 4096, 16384), (257, 1024, 16392), (300, 4096, 16384),
+                  # streaming without a split of K, and one K step
+                  (40, 4096, 16392), (7, 64, 2048), (200, 16, 8), (64, 128, 19000)]
 
 
 @pytest.mark.parametrize("M,K,N", PRODUCT_SHAPES)
@@ -252,7 +256,8 @@ def test_product_matches_the_definition(M, K, N):
 
 
 @pytest.mark.parametrize("bias", [False, True])
-@pytest.mark.parametrize("M,K,N", [(1, 512, 264), (30, 2048, 384), (150, 272, 136), (600, 512, 1000)])
+@pytest.mark.parametrize("M,K,N", [(1, 512, 264), (30, 2048, 384), (150, 272, 136), (600, 512, 1000),
+                                   (33, 256, 19000), (300, 4096, 16384)])
 def test_product_with_gelu(M, K, N, bias):
     _check_product(M, K, N, bias=bias, gelu=True, seed=M)
 
@@ -385,7 +390,134 @@ def test_two_layers_and_two_streams_at_once():
         assert torch.equal(a, b)
 
 
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements in x, the codes, the weight and y: the first and
+    the last rows."""
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB")
+    g = torch.Generator(device="cuda").manual_seed(70)
+    M, K = 65600, 32768
+    x = torch.zeros(M, K, dtype=BF16, device="cuda")
+    for part in (x[:3], x[-3:]):
+        part.copy_(torch.randn(3, K, generator=g, device="cuda"))
+    codes, scale = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    ll.ll_quantize_i8(x, M, K, codes, scale)
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    nc, ns = torch.empty_like(codes), torch.empty_like(scale)
+    ll.ll_rmsnorm_i8(x, x, None, 1e-6, M, K, h, y, nc, ns)
+    for rows in (slice(0, 4), slice(M - 4, M)):
+        xc = x[rows].cpu()
+        rc, a = i8ref.codes_of(xc)
+        assert torch.equal(codes[rows].cpu(), rc) and torch.equal(scale[rows].cpu(), a.float() / 127.0)
+        rh, ry, rc, rs = i8ref.rmsnorm(xc, xc, None, 1e-6)
+        assert torch.equal(h[rows].cpu(), rh) and torch.equal(nc[rows].cpu(), rc)
+        i8ref.check_y(y[rows], ry, i8ref.RSTD_TOL * ry.abs())
+        i8ref.check_scale(ns[rows], rs)
+    del x, codes, h, y, nc
+    # y of 2.3e9 elements
+    M, K, N = 140000, 64, 16392
+    xq, xs, wq, ws, b = _product_inputs(M, K, N, 71)
+    out = torch.empty(M, N, dtype=BF16, device="cuda")
+    _layer(wq, ws, b).forward(xq.cuda(), xs.cuda(), out=out)
+    for rows in (slice(0, 5), slice(M - 5, M)):
+        ref, size = i8ref.product(xq[rows], xs[rows], wq, ws, b, False)
+        i8ref.check_y(out[rows], ref, i8ref.PRODUCT_TOL * size)
+    del out
+    # a weight of 2.2e9 codes, on both kernels that stream it
+    N, K = 16904, 130000
+    wq = torch.randint(-127, 128, (N, K), generator=g, dtype=torch.int8, device="cuda")
+    ws = torch.rand(N, generator=g, device="cuda") * 1e-5
+    layer = ll.Int8LinearLayer(N, K)
+    layer.set_weights(wq, ws)
+    for M in (3, 300):
+        xq = torch.randint(-127, 128, (M, K), generator=g, dtype=torch.int8, device="cuda")
+        xs = torch.rand(M, generator=g, device="cuda")
+        got = layer.forward(xq, xs)
+        for cols in (slice(0, 9), slice(N - 9, N)):
+            ref, size = i8ref.product(xq.cpu(), xs.cpu(), wq[cols].cpu(), ws[cols].cpu(), None, False)
+            i8ref.check_y(got[:, cols], ref, i8ref.PRODUCT_TOL * size)
+    assert ll.ll_i8_status(layer.handle) == ll.LL_OK
+
+
+def test_tensors_of_other_strides_are_refused():
+    """Column slices, transposes, expanded rows: the library takes an address
+    only, so the binding refuses what is not contiguous."""
+    x = _rows(8, 128, 72).cuda()
+    c, s = torch.empty(8, 64, dtype=torch.int8, device="cuda"), torch.empty(8, device="cuda")
+    for bad in (x[:, :64], x[:, ::2], x.t()[:8], x[:1, :64].expand(8, 64), x[:, :64].float(), x[:, :64].cpu()):
+        with pytest.raises(ll.LLError) as e:
+            ll.ll_quantize_i8(bad, 8, 64, c, s)
+        assert e.value.code == ll.LL_ERR_INVALID_ARG
+    with pytest.raises(ll.LLError) as e:
+        ll.ll_rmsnorm_i8(x, None, x[:, 0], 1e-6, 8, 128, None, torch.empty_like(x), None, None)
+    assert e.value.code == ll.LL_ERR_INVALID_ARG
+    # a row slice is contiguous, and its address need only be 16-byte aligned
+    odd = torch.empty(8 * 128 + 8, dtype=BF16, device="cuda")[8:].view(8, 128)
+    odd.copy_(x)
+    c, s = torch.empty(8, 128, dtype=torch.int8, device="cuda"), torch.empty(9, device="cuda")[1:]
+    ll.ll_quantize_i8(odd, 8, 128, c, s)
+    assert torch.equal(c.cpu(), i8ref.codes_of(x.cpu())[0])
+
+
 # ------------------------------------------------------------------- chain
+def _block(M, K, F, seed):
+    """Buffers and layers of a feed-forward, and its step: the residual stream
+    in `h` takes the block's output."""
+    g = torch.Generator().manual_seed(seed)
+    up = ll.Int8LinearLayer.from_dense((torch.randn(F, K, generator=g) / math.sqrt(K)).to(BF16).cuda(),
+                                       epilogue=ll.LL_EPILOGUE_GELU_TANH)
+    down = ll.Int8LinearLayer.from_dense((torch.randn(K, F, generator=g) / math.sqrt(F)).to(BF16).cuda())
+    t = dict(h=_rows(M, K, seed).cuda(), d=_rows(M, K, seed + 1).cuda(), w=_rows(1, K, seed + 2, 0.0)[0].cuda(),
+             c1=torch.empty(M, K, dtype=torch.int8, device="cuda"), s1=torch.empty(M, device="cuda"),
+             mid=torch.empty(M, F, dtype=BF16, device="cuda"),
+             c2=torch.empty(M, F, dtype=torch.int8, device="cuda"), s2=torch.empty(M, device="cuda"))
+
+    def step(wait=lambda: None):
+        ll.ll_rmsnorm_i8(t["d"], t["h"], t["w"], 1e-6, M, K, t["h"], None, t["c1"], t["s1"])
+        wait()
+        up.forward(t["c1"], t["s1"], out=t["mid"])
+        wait()
+        ll.ll_quantize_i8(t["mid"], M, F, t["c2"], t["s2"])
+        wait()
+        down.forward(t["c2"], t["s2"], out=t["d"])
+        wait()
+
+    return t, step
+
+
+@pytest.mark.parametrize("M", [1, 48, 200, 700])
+def test_back_to_back_steps_equal_steps_one_by_one(M):
+    """Every kernel may start before the one ahead of it has ended, and each
+    step overwrites buffers that the step before still reads: 30 steps without a
+    wait, the same 30 captured in one graph, and 30 with a wait after every
+    call give the same bits."""
+    results = []
+    for mode in range(3):
+        t, step = _block(M, 512, 1536, 80)
+        torch.cuda.synchronize()
+        if mode == 0:
+            for _ in range(30):
+                step(torch.cuda.synchronize)
+        elif mode == 1:
+            for _ in range(30):
+                step()
+        else:
+            h0, d0 = t["h"].clone(), t["d"].clone()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                for _ in range(30):
+                    step()
+            t["h"].copy_(h0)
+            t["d"].copy_(d0)
+            g.replay()
+        torch.cuda.synchronize()
+        results.append((t["h"].cpu(), t["d"].cpu()))
+    for r in results[1:]:
+        assert torch.equal(r[0], results[0][0]) and torch.equal(r[1], results[0][1])
+    assert torch.isfinite(results[0][0].float()).all()
+
+
 @pytest.mark.parametrize("M", [1, 40, 333])
 def test_feed_forward_of_norm_product_quantisation_product(M):
     """The operators as a feed-forward uses them: residual + norm -> codes,
