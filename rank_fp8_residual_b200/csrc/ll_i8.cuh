@@ -172,22 +172,28 @@ __device__ __forceinline__ float4 ldg_ahead(const float4* p) {
   return v;
 }
 
+// Scales of the 16 tokens from m0 on (0 behind the last).
+__device__ __forceinline__ void i8_token_scales(float (&v)[16], const float* __restrict__ sx, int m0, int M) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    v[i] = 0.f;
+    if (m0 + i < M) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v[i]) : "l"(sx + m0 + i));
+  }
+}
+
 // Outputs of one feature (this lane's; s, b its scale and bias) for the 16
-// tokens from m0 on: a warp's lanes are 32 neighbouring features, 64 bytes of
-// a token's row.
+// tokens from m0 on, whose scales are sm: a warp's lanes are 32 neighbouring
+// features, 64 bytes of a token's row.
 template <int kAct>
-__device__ __forceinline__ void i8_store_tokens(const uint32_t (&v)[16], int m0, int M, int N, int f, float s, float b,
-                                                const float* __restrict__ sx, uint16_t* __restrict__ y) {
-  if (f >= N) return;
+__device__ __forceinline__ void i8_store_tokens(const uint32_t (&v)[16], const float (&sm)[16], int m0, int M, int N,
+                                                int f, float s, float b, uint16_t* __restrict__ y) {
   uint16_t* d = y + static_cast<size_t>(m0) * N + f;
 #pragma unroll
   for (int i = 0; i < 16; i += 2) {
-    if (m0 + i >= M) break;
-    const bool two = m0 + i + 1 < M;
-    const float a0 = __ldg(sx + m0 + i), a1 = two ? __ldg(sx + m0 + i + 1) : 0.f;
-    const uint32_t w = i8_out2<kAct>(static_cast<int>(v[i]), static_cast<int>(v[i + 1]), s, make_float4(a0, a1, b, b));
-    d[static_cast<size_t>(i) * N] = static_cast<uint16_t>(w);
-    if (two) d[static_cast<size_t>(i + 1) * N] = static_cast<uint16_t>(w >> 16);
+    const uint32_t w =
+        i8_out2<kAct>(static_cast<int>(v[i]), static_cast<int>(v[i + 1]), s, make_float4(sm[i], sm[i + 1], b, b));
+    if (f < N && m0 + i < M) d[static_cast<size_t>(i) * N] = static_cast<uint16_t>(w);
+    if (f < N && m0 + i + 1 < M) d[static_cast<size_t>(i + 1) * N] = static_cast<uint16_t>(w >> 16);
   }
 }
 
@@ -401,7 +407,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 #pragma unroll
         for (int i = 0; i < 16; ++i) sb[i] = ldg_ahead(sb4 + i);
       };
-      if (!kSwap && 32 * half < w) load_sb(32 * half);
+      float sx[16];  // kSwap: of the next chunk's tokens
+      if (kSwap)
+        i8_token_scales(sx, p.sx, b0 + 16 * half, p.M);
+      else if (32 * half < w)
+        load_sb(32 * half);
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], (it >> 1) & 1, p.watch, kErrTimeoutEpilogue))) break;
       tc_fence_after();
       const uint32_t acc = tl + 256u * buf;
@@ -409,7 +419,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
         for (int c = 16 * half; c < w && b0 + c < p.M; c += 32) {
           uint32_t v[16];
           tmem_ld16_wait(acc + c, v);
-          i8_store_tokens<kAct>(v, b0 + c, p.M, p.N, row, sm, bias, p.sx, p.y);
+          i8_store_tokens<kAct>(v, sx, b0 + c, p.M, p.N, row, sm, bias, p.y);
+          if (c + 32 < w) i8_token_scales(sx, p.sx, b0 + c + 32, p.M);
         }
       } else {
         for (int c = 32 * half; c < w; c += 64) {
@@ -585,6 +596,8 @@ __global__ void __launch_bounds__(kIsThreads, 1) ll_i8_stream_kernel(const __gri
     const float4 s2 = f < p.N ? __ldg(p.sb + f / 2) : make_float4(0.f, 0.f, 0.f, 0.f);
     const float s = f & 1 ? s2.y : s2.x, b = f & 1 ? s2.w : s2.z;
     int* part = reinterpret_cast<int*>(ring) + 32 * q + lane;
+    float sx[16];  // of the next block's tokens
+    if (p.splits == 1) i8_token_scales(sx, p.sx, 16 * half, p.M);
     if (__all_sync(0xffffffffu, mbar_wait(acc_full, 0, p.watch, kErrTimeoutEpilogue))) {
       tc_fence_after();
       for (int c = 16 * half; c < p.Mt; c += 32) {
@@ -594,7 +607,8 @@ __global__ void __launch_bounds__(kIsThreads, 1) ll_i8_stream_kernel(const __gri
 #pragma unroll
           for (int i = 0; i < 16; ++i) part[(c + i) * 128] = static_cast<int>(v[i]);
         } else {
-          i8_store_tokens<kAct>(v, c, p.M, p.N, f, s, b, p.sx, p.y);
+          i8_store_tokens<kAct>(v, sx, c, p.M, p.N, f, s, b, p.y);
+          i8_token_scales(sx, p.sx, c + 32, p.M);
         }
       }
     } else {
