@@ -115,12 +115,19 @@ def _addr(t):
     return t.data_ptr()
 
 
+_raw_stream = _raw_device = None
+
+
 def _stream(s):
     if s is None:
-        # torch.cuda.current_stream().cuda_stream without the Stream object
-        # (0.2 against 3.2 us, which a one-token call would feel)
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # What torch.cuda.current_stream().cuda_stream gives, without the
+        # Stream object (0.2 against 3.2 us, which a one-token call would feel).
+        global _raw_stream, _raw_device
+        if _raw_stream is None:
+            import torch
+            torch.cuda.current_device()  # initialises CUDA
+            _raw_stream, _raw_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        return _raw_stream(_raw_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -285,15 +292,16 @@ def _load_dtypes():
     _BF16, _INT8, _F32 = torch.bfloat16, torch.int8, torch.float32
 
 
-def _buffer(t, what, dtype, shape):
+def _buffer(t, what, dtype, n):
     """Address of an argument of the int8 operators.  A tensor has to be
-    contiguous CUDA memory of that type and shape (the library sees only its
-    address); an integer address is taken as it is."""
+    contiguous CUDA memory of that type with n elements (the library sees only
+    its address, so leading dimensions may be split as the caller likes); an
+    integer address is taken as it is."""
     if t is None or type(t) is int:
         return t
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+    if t.dtype is dtype and t.numel() == n and t.is_cuda and t.is_contiguous():
         return t.data_ptr()
-    raise LLError(LL_ERR_INVALID_ARG, f"{what}: a contiguous CUDA tensor of {dtype} and shape {shape} is needed, "
+    raise LLError(LL_ERR_INVALID_ARG, f"{what}: a contiguous CUDA tensor of {dtype} with {n} elements is needed, "
                                       f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
@@ -307,11 +315,10 @@ def ll_rmsnorm_i8(x, residual, weight, eps: float, M: int, K: int, h, y, codes, 
     if _BF16 is None:
         _load_dtypes()
     M, K, b = int(M), int(K), _BF16
-    mk = (M, K)
-    rc = _lib.ll_rmsnorm_i8(_buffer(x, "x", b, mk), _buffer(residual, "residual", b, mk),
-                            _buffer(weight, "weight", b, (K,)), eps, M, K, _buffer(h, "h", b, mk),
-                            _buffer(y, "y", b, mk), _buffer(codes, "codes", _INT8, mk),
-                            _buffer(scale, "scale", _F32, (M,)), _stream(stream))
+    n = M * K
+    rc = _lib.ll_rmsnorm_i8(_buffer(x, "x", b, n), _buffer(residual, "residual", b, n),
+                            _buffer(weight, "weight", b, K), eps, M, K, _buffer(h, "h", b, n), _buffer(y, "y", b, n),
+                            _buffer(codes, "codes", _INT8, n), _buffer(scale, "scale", _F32, M), _stream(stream))
     if rc != LL_OK:
         raise LLError(rc, "ll_rmsnorm_i8")
 
@@ -322,9 +329,9 @@ def ll_quantize_i8(x, M: int, K: int, codes, scale, stream=None) -> None:
     if _BF16 is None:
         _load_dtypes()
     M, K = int(M), int(K)
-    mk = (M, K)
-    rc = _lib.ll_quantize_i8(_buffer(x, "x", _BF16, mk), M, K, _buffer(codes, "codes", _INT8, mk),
-                             _buffer(scale, "scale", _F32, (M,)), _stream(stream))
+    n = M * K
+    rc = _lib.ll_quantize_i8(_buffer(x, "x", _BF16, n), M, K, _buffer(codes, "codes", _INT8, n),
+                             _buffer(scale, "scale", _F32, M), _stream(stream))
     if rc != LL_OK:
         raise LLError(rc, "ll_quantize_i8")
 
@@ -380,9 +387,9 @@ def ll_i8_destroy(h: int) -> None:
 
 class Int8LinearLayer:
     """Owns one int8 layer: y = bf16(act(scale[m] * w_scale[n] * (codes
-    w_codes^T) + bias)).  ``forward(codes, scale)`` takes the int8 codes [M, K]
-    and float32 scale [M] of ll_rmsnorm_i8 or ll_quantize_i8 and returns a new
-    bf16 tensor [M, N] (or ``out``)."""
+    w_codes^T) + bias)).  ``forward(codes, scale)`` takes the int8 codes [..., K]
+    and float32 scale [...] of ll_rmsnorm_i8 or ll_quantize_i8 and returns a new
+    bf16 tensor [..., N] (or ``out``)."""
 
     def __init__(self, N: int, K: int, epilogue: int = LL_EPILOGUE_NONE):
         self.handle = None
@@ -394,8 +401,8 @@ class Int8LinearLayer:
     def set_weights(self, codes, scale, bias=None):
         """codes int8 [N, K], scale float32 [N], bias bf16 [N] or None (CUDA)."""
         _load_dtypes()
-        ll_i8_set_weights(self.handle, _buffer(codes, "codes", _INT8, (self.N, self.K)),
-                          _buffer(scale, "scale", _F32, (self.N,)), _buffer(bias, "bias", _BF16, (self.N,)))
+        ll_i8_set_weights(self.handle, _buffer(codes, "codes", _INT8, self.N * self.K),
+                          _buffer(scale, "scale", _F32, self.N), _buffer(bias, "bias", _BF16, self.N))
 
     @classmethod
     def from_dense(cls, W, bias=None, epilogue: int = LL_EPILOGUE_NONE):
@@ -413,12 +420,14 @@ class Int8LinearLayer:
     def forward(self, codes, scale, out=None, stream=None):
         if _BF16 is None:
             _load_dtypes()
-        M = codes.shape[0]
+        M = scale.numel()
         if out is None:
             import torch
-            out = torch.empty(M, self.N, dtype=_BF16, device=codes.device)
-        ll_i8_forward(self.handle, _buffer(codes, "codes", _INT8, (M, self.K)), _buffer(scale, "scale", _F32, (M,)),
-                      _buffer(out, "out", _BF16, (M, self.N)), M, stream)
+            out = torch.empty(*scale.shape, self.N, dtype=_BF16, device=codes.device)
+        rc = _lib.ll_i8_forward(self.handle, _buffer(codes, "codes", _INT8, M * self.K), _buffer(scale, "scale", _F32, M),
+                                _buffer(out, "out", _BF16, M * self.N), M, _stream(stream))
+        if rc != LL_OK:
+            raise LLError(rc, "ll_i8_forward")
         return out
 
     def close(self):

@@ -452,6 +452,13 @@ def test_tensors_of_other_strides_are_refused():
     with pytest.raises(ll.LLError) as e:
         ll.ll_rmsnorm_i8(x, None, x[:, 0], 1e-6, 8, 128, None, torch.empty_like(x), None, None)
     assert e.value.code == ll.LL_ERR_INVALID_ARG
+    # leading dimensions may be split: batch x sequence
+    layer = _layer(*_product_inputs(1, 128, 24, 73)[2:])
+    c, s = torch.empty(2, 4, 128, dtype=torch.int8, device="cuda"), torch.empty(2, 4, device="cuda")
+    ll.ll_quantize_i8(x.view(2, 4, 128), 8, 128, c, s)
+    y = layer.forward(c, s)
+    assert y.shape == (2, 4, 24)
+    assert torch.equal(y.view(8, 24), layer.forward(c.view(8, 128), s.view(8)))
     # a row slice is contiguous, and its address need only be 16-byte aligned
     odd = torch.empty(8 * 128 + 8, dtype=BF16, device="cuda")[8:].view(8, 128)
     odd.copy_(x)
