@@ -385,8 +385,8 @@ int ll_forward_noalloc(const void *x, const void *A, const void *B, const void *
  * output may overlap an input or another output.  u is the exact product
  * (it fits binary32), and the codes are the exact rounding of the quotient:
  * they have one right value.  A row of zeros has codes and scale 0; a row
- * in which some u is NaN or infinite has codes 0 and scale NaN.  Sums and
- * rstd are binary32; squares that overflow it are summed scaled, so every
+ * in which some u is NaN or infinite has codes 0 and scale NaN (its y is what
+ * the formula gives).  Sums and rstd are binary32; squares that overflow it are summed scaled, so every
  * finite row has its norm.  eps >= 1e-30.  M == 0 is a no-op.
  * Errors: LL_ERR_INVALID_ARG for bad sizes or eps, null / misaligned
  * (16 bytes; scale 4) / overlapping pointers or pointers that are not memory

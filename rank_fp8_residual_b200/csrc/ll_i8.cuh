@@ -138,14 +138,15 @@ __device__ __forceinline__ float rcp(float v) {
   return d;
 }
 
-// Two neighbouring outputs of a token from their sums: sm is the token's
-// scale, s = (scale, scale, bias, bias) of the two features.  GELU:
+// Two outputs from their sums: first scaled by sm, then s = (scale, scale, bias,
+// bias).  The sum takes one scale after the other, as the formula's factors may
+// be far from 1 where their product with it is not.  GELU:
 // v / 2 (1 + tanh(z)) = v / (1 + exp(-2 z)), z = sqrt(2 / pi) (v + 0.044715 v^3);
 // exp(-2 z) as a power of two: -2 z log2(e) = v (-2.3022082 - 0.10294324 v^2).
 template <int kAct>
 __device__ __forceinline__ uint32_t i8_out2(int a0, int a1, float sm, const float4& s) {
-  float2 v = fma2(mul2(make_float2(s.x, s.y), make_float2(sm, sm)),
-                  make_float2(static_cast<float>(a0), static_cast<float>(a1)), make_float2(s.z, s.w));
+  float2 v = fma2(mul2(make_float2(static_cast<float>(a0), static_cast<float>(a1)), make_float2(sm, sm)),
+                  make_float2(s.x, s.y), make_float2(s.z, s.w));
   if constexpr (kAct == kActGelu) {
     const float2 t = mul2(v, fma2(mul2(v, v), make_float2(-0.10294324f, -0.10294324f),
                                   make_float2(-2.3022082f, -2.3022082f)));

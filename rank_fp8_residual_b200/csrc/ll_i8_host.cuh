@@ -19,6 +19,7 @@ struct ll_i8_layer {
   int N_pad = 0;         // room for a tile of 256 features that starts at the last one
   int* status = nullptr;
   int clusters[llk::kIsMaxSplit + 1] = {};  // co-resident clusters of that many CTAs of the streaming kernel
+  int pairs = 0;                            // co-resident CTA pairs of the pair kernel
   int epilogue = LL_EPILOGUE_NONE;
   int withhold = 0;
   uint64_t timeout_ns = 2000000000ull;
@@ -125,6 +126,13 @@ bool setup_i8(ll_i8_layer* h) {
       return false;
   }
   h->clusters[1] = h->num_sms;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(h->num_sms);
+  cfg.blockDim = dim3(kI8Threads);
+  cfg.dynamicSmemBytes = i8_smem_bytes();
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel_i8(LL_EPILOGUE_NONE, false), &cfg) != cudaSuccess || n < 1) return false;
+  h->pairs = std::min(n, h->num_sms / 2);
   return true;
 }
 
@@ -155,7 +163,7 @@ struct I8Plan {
 double i8_weight_cycles(const ll_i8_layer* h) { return static_cast<double>(h->N) * h->K * 3.07e-4; }
 
 I8Plan i8_plan_pair(const ll_i8_layer* h, int M) {
-  const int pairs = h->num_sms / 2;
+  const int pairs = h->pairs;
   const double steps = (h->K + 127) / 128;
   I8Plan best{};
   best.cycles = -1;
@@ -262,7 +270,7 @@ int launch_i8(const ll_i8_layer* h, const I8Plan& plan, const void* codes, const
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long long>(tiles, h->num_sms / 2)));
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long long>(tiles, h->pairs)));
   cfg.blockDim = dim3(kI8Threads);
   cfg.dynamicSmemBytes = i8_smem_bytes();
   cfg.stream = st;
@@ -467,6 +475,7 @@ int ll_i8_plan(int N, int K, int M, int num_sms, int* kernel, int* tile_features
   view.N = N;
   view.K = K;
   view.num_sms = num_sms;
+  view.pairs = num_sms / 2;
   for (int s = 1; s <= llk::kIsMaxSplit; ++s) view.clusters[s] = num_sms / s;
   const I8Plan p = i8_plan(&view, M);
   if (kernel) *kernel = p.stream ? LL_I8_STREAM : p.swap ? LL_I8_PAIR_SWAP : LL_I8_PAIR;

@@ -293,6 +293,21 @@ def test_a_nan_scale_gives_a_row_of_nan_and_touches_no_other(M):
     assert torch.equal(y[keep], want[keep])
 
 
+@pytest.mark.parametrize("M", [2, 100, 300, 700])
+def test_scales_far_from_one(M):
+    """Scales whose product leaves binary32 although every output is in range,
+    and sums of zero under scales whose product is infinite."""
+    xq, xs, wq, ws, _ = _product_inputs(M, 256, 520, 34)
+    xq[0] = 0
+    xs = torch.where(torch.arange(M) % 2 == 0, 1e30, 1e-25) * (xs + 1)
+    ws = torch.where(torch.arange(520) % 2 == 0, 1e25, 1e-30) * (ws.abs() + 1)
+    y = _forward(_layer(wq, ws, None), xq, xs).cpu()
+    ref, size = i8ref.product(xq, xs, wq, ws, None, False)
+    seen = (ref.abs() < 1e38) & ((ref == 0) | (ref.abs() > 1e-35))
+    assert seen.float().mean() > 0.4 and torch.all(y[0] == 0)
+    i8ref.check_y(y[seen], ref[seen], i8ref.PRODUCT_TOL * size[seen])
+
+
 def test_layer_refusals():
     xq, xs, wq, ws, b = (t.cuda() for t in _product_inputs(4, 64, 16, 32))
     layer = ll.Int8LinearLayer(16, 64)
