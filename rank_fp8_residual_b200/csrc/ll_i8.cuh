@@ -22,121 +22,11 @@
 
 #include "ll_kernels.cuh"
 #include "ptx.cuh"
+#include "ptx_i8.cuh"
 
 namespace llk {
 
 constexpr int kI8MaxK = 131056;
-
-// Instruction descriptor of tcgen05.mma kind::i8: int32 accumulation, signed
-// A and B, both K-major.
-__host__ __device__ __forceinline__ constexpr uint32_t idesc_i8(int m, int n) {
-  return (2u << 4)                                  // D format: s32
-         | (1u << 7)                                // A format: s8
-         | (1u << 10)                               // B format: s8
-         | (static_cast<uint32_t>(n >> 3) << 17)    // N / 8
-         | (static_cast<uint32_t>(m >> 4) << 24);   // M / 16
-}
-
-// MMAs, commits and tile loads are issued by one lane of a warp whose control
-// flow stays uniform: with the descriptors in warp-uniform registers an MMA of
-// 256 x 64 issues every 45 cycles with a commit after every four (65 with a
-// barrier poll too); from inside an `if (lane == 0)` it took 110, whatever its
-// size.  `one` is elect_one()'s.
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one)
-      : "memory");
-}
-__device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one)
-      : "memory");
-}
-__device__ __forceinline__ void commit_one(uint64_t* bar, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-      "r"(one)
-      : "memory");
-}
-__device__ __forceinline__ void commit_one_pair(uint64_t* bar, uint16_t cta_mask, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
-      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
-          smem_u32(bar)),
-      "h"(cta_mask), "r"(one)
-      : "memory");
-}
-
-__device__ __forceinline__ void expect_one(uint64_t* bar, uint32_t bytes, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
-      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
-      "r"(bytes), "r"(one)
-      : "memory");
-}
-// Tile loads into shared memory, completing on a barrier of this CTA, or (pair)
-// on one of either CTA of the pair, given by its cluster address.
-__device__ __forceinline__ void load_2d_one(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1,
-                                            uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %5, 0;\n\t"
-      "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::
-          "r"(dst),
-      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(one)
-      : "memory");
-}
-__device__ __forceinline__ void load_3d_one(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
-                                            uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %6, 0;\n\t"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-      "[%2];\n\t}" ::"r"(dst),
-      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(one)
-      : "memory");
-}
-__device__ __forceinline__ void load_2d_pair_one(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1,
-                                                 uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %5, 0;\n\t"
-      "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
-      "%4}], [%2];\n\t}" ::"r"(dst),
-      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(one)
-      : "memory");
-}
-__device__ __forceinline__ void load_3d_pair_one(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1,
-                                                 int c2, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %6, 0;\n\t"
-      "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
-      "%4, %5}], [%2];\n\t}" ::"r"(dst),
-      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(one)
-      : "memory");
-}
-
-__device__ __forceinline__ float ex2(float v) {
-  float d;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
-  return d;
-}
-__device__ __forceinline__ float rcp(float v) {
-  float d;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
-  return d;
-}
 
 // Two outputs from their sums: first scaled by sm, then s = (scale, scale, bias,
 // bias).  The sum takes one scale after the other, as the formula's factors may
@@ -155,30 +45,12 @@ __device__ __forceinline__ uint32_t i8_out2(int a0, int a1, float sm, const floa
   return pack_bf16x2(v.x, v.y);
 }
 
-// The tile's store to y and its bulk group, by the lane for which `one` holds.
-__device__ __forceinline__ void store_2d_one(const CUtensorMap* m, uint32_t src, int c0, int c1, bool in, bool one) {
-  asm volatile(
-      "{\n\t.reg .pred e, f;\n\tsetp.ne.b32 e, %4, 0;\n\tsetp.ne.b32 f, %5, 0;\n\t"
-      "@e cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
-      "@f cp.async.bulk.commit_group;\n\t}" ::"l"(m),
-      "r"(src), "r"(c0), "r"(c1), "r"(static_cast<uint32_t>(in && one)), "r"(static_cast<uint32_t>(one))
-      : "memory");
-}
-
-// A read-only load that stays where it stands: ahead of a wait whose time covers
-// its latency.
-__device__ __forceinline__ float4 ldg_ahead(const float4* p) {
-  float4 v;
-  asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
-  return v;
-}
-
 // Scales of the 16 tokens from m0 on (0 behind the last).
-__device__ __forceinline__ void i8_token_scales(float (&v)[16], const float* __restrict__ sx, int m0, int M) {
+__device__ __forceinline__ void i8_token_scales(float (&v)[16], const float* sx, int m0, int M) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     v[i] = 0.f;
-    if (m0 + i < M) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v[i]) : "l"(sx + m0 + i));
+    if (m0 + i < M) v[i] = ld_ahead(sx + m0 + i);
   }
 }
 
@@ -400,7 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
           bias = row & 1 ? s2.w : s2.z;
         }
       } else if (row < p.M) {
-        sm = __ldg(p.sx + row);
+        sm = ld_ahead(p.sx + row);
       }
       float4 sb[16];  // of the next chunk's features
       auto load_sb = [&](int c) {
@@ -631,7 +503,7 @@ __global__ void __launch_bounds__(kIsThreads, 1) ll_i8_stream_kernel(const __gri
     const float4 s0v = __ldg(p.sb + (f0 + c) / 2), s1v = __ldg(p.sb + (f0 + c) / 2 + 1);
     const uint32_t part = smem_u32(ring) + 4 * c;
     for (int m = z + warp * p.splits; m < p.M; m += (kIsThreads / 32) * p.splits) {
-      const float sm = __ldg(p.sx + m);
+      const float sm = ld_ahead(p.sx + m);
       int4 v[kIsMaxSplit];
 #pragma unroll
       for (int r = 0; r < kIsMaxSplit; ++r)

@@ -29,6 +29,7 @@
 #include <cuda.h>
 
 #include "ptx.cuh"
+#include "ptx_i8.cuh"
 
 namespace llk {
 
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(rows_max_threads(kC, kKeep), kC <= 2 ? 1 : 0) 
       rv[j] = c < nv ? reinterpret_cast<const uint4*>(p.residual + row)[c] : make_uint4(0, 0, 0, 0);
   }
   const auto gain = [&](int c) {
-    return c < nv ? __ldg(reinterpret_cast<const uint4*>(p.w) + c) : make_uint4(kOnes, kOnes, kOnes, kOnes);
+    return c < nv ? reinterpret_cast<const uint4*>(p.w)[c] : make_uint4(kOnes, kOnes, kOnes, kOnes);
   };
   constexpr bool kAhead = kC <= 4;  // the gains' loads go out with x's
   uint4 wv[kAhead ? kC : 1];
