@@ -18,6 +18,7 @@ struct ll_i8_layer {
   float4* sb = nullptr;  // [N_pad / 2] (scale, scale, bias, bias), zeros behind the last feature
   int N_pad = 0;         // room for a tile of 256 features that starts at the last one
   int* status = nullptr;
+  CUtensorMap tm_w[7];   // maps of W with boxes of 32, 48 .. 128 rows (half of the pair kernel's widths)
   int clusters[llk::kIsMaxSplit + 1] = {};  // co-resident clusters of that many CTAs of the streaming kernel
   int pairs = 0;                            // co-resident CTA pairs of the pair kernel
   int epilogue = LL_EPILOGUE_NONE;
@@ -136,10 +137,14 @@ bool setup_i8(ll_i8_layer* h) {
   return true;
 }
 
-bool make_weight_map(const ll_i8_layer* h, CUtensorMap* m, int rows) {
-  return make_map3(m, h->W, CU_TENSOR_MAP_DATA_TYPE_UINT8, 128, h->N, (h->K + 127) / 128, 128,
-                   128ull * h->N, 128, static_cast<uint32_t>(rows), 1, CU_TENSOR_MAP_SWIZZLE_128B);
+bool make_weight_maps(ll_i8_layer* h) {
+  for (int i = 0; i < 7; ++i)
+    if (!make_map3(&h->tm_w[i], h->W, CU_TENSOR_MAP_DATA_TYPE_UINT8, 128, h->N, (h->K + 127) / 128, 128, 128ull * h->N,
+                   128, 32 + 16 * i, 1, CU_TENSOR_MAP_SWIZZLE_128B))
+      return false;
+  return true;
 }
+const CUtensorMap& weight_map(const ll_i8_layer* h, int rows) { return h->tm_w[(rows - 32) / 16]; }
 
 constexpr int kI8StreamMaxM = 256;  // the MMA's N
 
@@ -209,9 +214,9 @@ int launch_i8_stream(const ll_i8_layer* h, const I8Plan& plan, const void* codes
   using namespace llk;
   I8StreamParams p;
   p.Mt = (M + 15) / 16 * 16;
-  if (!make_map(&p.tm_x, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, M, h->K, h->K, 128, p.Mt, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_weight_map(h, &p.tm_w, 128))
+  if (!make_map(&p.tm_x, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, M, h->K, h->K, 128, p.Mt, CU_TENSOR_MAP_SWIZZLE_128B))
     return LL_ERR_CUDA;
+  p.tm_w = weight_map(h, 128);
   p.sx = scale;
   p.sb = h->sb;
   p.y = static_cast<uint16_t*>(y);
@@ -254,9 +259,9 @@ int launch_i8(const ll_i8_layer* h, const I8Plan& plan, const void* codes, const
   p.w = plan.w;
   if (!make_map(&p.tm_x, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, M, h->K, h->K, 128, plan.swap ? p.w / 2 : 128,
                 CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_weight_map(h, &p.tm_w, plan.swap ? 128 : p.w / 2) ||
-      !make_map(&p.tm_y, y, kBF16, M, h->N, 2ull * h->N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+      (!plan.swap && !make_map(&p.tm_y, y, kBF16, M, h->N, 2ull * h->N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)))
     return LL_ERR_CUDA;
+  p.tm_w = weight_map(h, plan.swap ? 128 : p.w / 2);
   p.sx = scale;
   p.sb = h->sb;
   p.y = static_cast<uint16_t*>(y);
@@ -295,9 +300,9 @@ int ll_rmsnorm_i8(const void* x, const void* residual, const void* weight, float
   g_last_error = LL_OK;
   if (M < 0 || K < 16 || K % 16 != 0 || !std::isfinite(eps) || eps < 1e-30f) return fail(LL_ERR_INVALID_ARG);
   if (K > llk::kRowsMaxK) return fail(LL_ERR_UNSUPPORTED);
-  if ((codes == nullptr) != (scale == nullptr) || (!codes && !y) || (h && !residual)) return fail(LL_ERR_INVALID_ARG);
   if (M == 0) return LL_OK;
-  if (!x) return fail(LL_ERR_INVALID_ARG);
+  if (!x || (codes == nullptr) != (scale == nullptr) || (!codes && !y) || (h && !residual))
+    return fail(LL_ERR_INVALID_ARG);
   if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(h, 16) || !aligned(y, 16) ||
       !aligned(codes, 16) || !aligned(scale, 4))
     return fail(LL_ERR_INVALID_ARG);
@@ -388,7 +393,7 @@ ll_i8_handle ll_i8_create(int N, int K) {
     fail(LL_ERR_OOM);
     return nullptr;
   }
-  if (!setup_i8(h) || !encode_fn() || cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess ||
+  if (!setup_i8(h) || !encode_fn() || !make_weight_maps(h) || cudaMemset(h->status, 0, sizeof(int)) != cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess) {
     cudaGetLastError();
     free_i8(h);

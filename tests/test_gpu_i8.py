@@ -455,6 +455,16 @@ def test_offsets_beyond_32_bits():
     assert ll.ll_i8_status(layer.handle) == ll.LL_OK
 
 
+def test_empty_batches():
+    x, c, s = torch.empty(0, 64, dtype=BF16, device="cuda"), torch.empty(0, 64, dtype=torch.int8, device="cuda"), \
+        torch.empty(0, device="cuda")
+    ll.ll_rmsnorm_i8(x, x, None, 1e-6, 0, 64, x, x, c, s)
+    ll.ll_quantize_i8(x, 0, 64, c, s)
+    layer = _layer(*_product_inputs(1, 64, 24, 74)[2:])
+    assert layer.forward(c, s).shape == (0, 24)
+    assert layer.forward(c.view(0, 5, 64), s.view(0, 5)).shape == (0, 5, 24)
+
+
 def test_tensors_of_other_strides_are_refused():
     """Column slices, transposes, expanded rows: the library takes an address
     only, so the binding refuses what is not contiguous."""

@@ -36,6 +36,7 @@ def test_norm_refuses(change):
 def test_norm_row_limit_and_empty_batch():
     assert _code(lambda: _norm(K=65552)) == ll.LL_ERR_UNSUPPORTED
     _norm(M=0)
+    _norm(M=0, x=None, codes=None, scale=None)  # an empty tensor's address is null
     ll.ll_quantize_i8(A, 0, 64, C, D, 0)
     assert _code(ll.ll_quantize_i8, A, 4, 65552, C, D, 0) == ll.LL_ERR_UNSUPPORTED
 
