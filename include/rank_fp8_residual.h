@@ -382,12 +382,15 @@ int ll_forward_noalloc(const void *x, const void *A, const void *B, const void *
  * [M, K]; scale fp32 [M].  residual, weight, h and y may be NULL, and codes
  * together with scale; one of y and codes must be asked for, and h only
  * with a residual.  h may be x or residual itself (in place); no other
- * output may overlap an input or another output.  u is the exact product
- * (it fits binary32), and the codes are the exact rounding of the quotient:
- * they have one right value.  A row of zeros has codes and scale 0; a row
- * in which some u is NaN or infinite has codes 0 and scale NaN (its y is what
- * the formula gives).  Sums and rstd are binary32; squares that overflow it are summed scaled, so every
- * finite row has its norm.  eps >= 1e-30.  M == 0 is a no-op.
+ * output may overlap an input or another output.  u is the exact product,
+ * and the codes are the exact rounding of the quotient: they have one right
+ * value.  A row of zeros has codes and scale 0; a row in which some u is NaN
+ * or infinite has codes 0 and scale NaN (its y is what the formula gives).
+ * Sums and rstd are binary32; a row whose squares or products overflow it, or
+ * whose products are all below 2^-100, is taken in binary64, so every finite
+ * row has its norm.  (Products below 2^-126 beside larger ones are rounded as
+ * binary32 rounds them: their codes are 0.)  A scale or y beyond its type is
+ * infinite.  eps >= 1e-30.  M == 0 is a no-op.
  * Errors: LL_ERR_INVALID_ARG for bad sizes or eps, null / misaligned
  * (16 bytes; scale 4) / overlapping pointers or pointers that are not memory
  * of the current device; LL_ERR_UNSUPPORTED for K > 65536; LL_ERR_CUDA. */

@@ -58,7 +58,10 @@ cudaError_t launch_rows_i8_as(const llk::RowsParams& p, int chunks, bool keep, c
       if constexpr (kNorm)
         if (keep) return cudaLaunchKernelEx(&cfg, ll_rows_i8_kernel<4, true, true>, p);
       return cudaLaunchKernelEx(&cfg, ll_rows_i8_kernel<4, kNorm, false>, p);
-    default: return cudaLaunchKernelEx(&cfg, ll_rows_i8_kernel<8, kNorm, false>, p);
+    default:
+      if constexpr (kNorm)
+        if (keep) return cudaLaunchKernelEx(&cfg, ll_rows_i8_kernel<8, true, true>, p);
+      return cudaLaunchKernelEx(&cfg, ll_rows_i8_kernel<8, kNorm, false>, p);
   }
 }
 
@@ -69,7 +72,13 @@ int launch_rows_i8(const llk::RowsParams& p, bool norm, int sms, cudaStream_t st
   // Norm with residual, us with 1 / 2 / 4 chunks: 100 x 8192 2.8 / 3.2 / 3.2,
   // 400 x 4096 5.0 / 3.9 / 4.2, 3630 x 4096 29.2 / 19.9 / 18.0, 16384 x 4096
   // 118 / 78 / 69.  Eight where four would need more than 1024 threads.
+  // Without a residual there is half as much to load beside the same work, and
+  // the reductions count: long rows take eight chunks by half the warps (us
+  // with 4 / 8: 1400 x 8192 11.4 / 11.1, 6000 x 8192 35.5 / 32.5, 16384 x 8192
+  // 89.8 / 80.7, 5000 x 6144 23.0 / 22.5; but 16384 x 4096 41.0 / 42.3, and
+  // with a residual 16384 x 8192 134 / 137).
   int c = p.M <= 2 * sms ? 1 : (p.M <= 8 * sms && nv <= 512 ? 2 : 4);
+  if (norm && !p.residual && c == 4 && p.M > 8 * sms && nv > 640 && nv <= 1024) c = 8;
   while (c < 8 && nv > 1024 * c) c *= 2;
   while (c > 1 && nv <= 16 * c) c /= 2;
   const int threads = ((nv + c - 1) / c + 31) / 32 * 32;
@@ -84,7 +93,8 @@ int launch_rows_i8(const llk::RowsParams& p, bool norm, int sms, cudaStream_t st
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((norm ? launch_rows_i8_as<true>(p, c, threads <= 256, cfg) : launch_rows_i8_as<false>(p, c, false, cfg)) == cudaSuccess) return LL_OK;
+  const bool keep = threads <= llk::rows_max_threads(c, true);
+  if ((norm ? launch_rows_i8_as<true>(p, c, keep, cfg) : launch_rows_i8_as<false>(p, c, false, cfg)) == cudaSuccess) return LL_OK;
   cudaGetLastError();
   return LL_ERR_CUDA;
 }

@@ -27,6 +27,7 @@
 #pragma once
 #include <cstdint>
 #include <cuda.h>
+#include <math_constants.h>
 
 #include "ptx.cuh"
 #include "ptx_i8.cuh"
@@ -47,13 +48,24 @@ struct RowsParams {
 
 constexpr float kRound = 12582912.f;  // 1.5 * 2^23
 constexpr int kRowsMaxK = 1024 * 8 * 8;  // 1024 threads with 8 chunks of 8 values each
-// Threads per row that a kernel may have: 1024, or 256 for four chunks per
-// thread with u kept.
-constexpr int rows_max_threads(int c, bool keep) { return c == 4 && keep ? 256 : 1024; }
+// Threads per row that a kernel may have: 1024, or as many as 8192 values need
+// for four and eight chunks per thread with u kept.
+constexpr int rows_max_threads(int c, bool keep) { return c >= 4 && keep ? 1024 / c : 1024; }
 
 // The two bf16 of a word.
 __device__ __forceinline__ float2 bf16x2_to_f32x2(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+// The two products of the bf16 of two words, exact in binary32 (-0 added keeps
+// a zero's sign), by the multiplier that takes bf16 operands as they lie
+// (16384 x 4096 without residual 41.3 us with the gain unpacked, 40.4 so).
+__device__ __forceinline__ float2 mul_bf16x2(uint32_t a, uint32_t b) {
+  float2 r;
+  asm("{\n\t.reg .b16 al, ah, bl, bh;\n\tmov.b32 {al, ah}, %2;\n\tmov.b32 {bl, bh}, %3;\n\t"
+      "fma.rn.f32.bf16 %0, al, bl, 0f80000000;\n\tfma.rn.f32.bf16 %1, ah, bh, 0f80000000;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(a), "r"(b));
+  return r;
 }
 constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones
 // Two maxima of magnitudes, NaN where either is.
@@ -86,21 +98,95 @@ __device__ __forceinline__ uint32_t pack_codes(float2 a, float2 b) {
                      __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
 
+// The norm of a row that leaves binary32's range: squares or products that
+// overflow (finite ones are finite here, below 2^256), products all below
+// 2^-100 (the largest then has too few bits to spare: exact here), NaN and
+// infinities, which are marked.  In binary64, where 127 u is exact and the
+// quotient's rounding cannot cross n + 1/2.  h comes from memory once more:
+// as this thread stored it, or from inputs that nothing has written.  A row
+// of zeros under a gain comes here too (3630 x 4096 of nothing else 34 us,
+// ordinary rows 17).
+__device__ __forceinline__ void norm_row_far(const RowsParams& p, int m) {
+  __shared__ double s_far[2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5, nv = p.K >> 3;
+  const size_t row = static_cast<size_t>(m) * p.K;
+  const auto load = [&](int c, uint32_t* hw, uint32_t* ww) {
+    uint4 v = reinterpret_cast<const uint4*>((p.h ? p.h : p.x) + row)[c];
+    if (p.residual && !p.h) {
+      const uint4 r = reinterpret_cast<const uint4*>(p.residual + row)[c];
+      v = make_uint4(add_bf16x2(v.x, r.x), add_bf16x2(v.y, r.y), add_bf16x2(v.z, r.z), add_bf16x2(v.w, r.w));
+    }
+    const uint4 w = p.w ? reinterpret_cast<const uint4*>(p.w)[c] : make_uint4(kOnes, kOnes, kOnes, kOnes);
+    hw[0] = v.x, hw[1] = v.y, hw[2] = v.z, hw[3] = v.w;
+    ww[0] = w.x, ww[1] = w.y, ww[2] = w.z, ww[3] = w.w;
+  };
+  double ss = 0., a = 0.;
+  for (int c = threadIdx.x; c < nv; c += blockDim.x) {
+    uint32_t hw[4], ww[4];
+    load(c, hw, ww);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 h = bf16x2_to_f32x2(hw[i]), w = bf16x2_to_f32x2(ww[i]);
+      ss += static_cast<double>(h.x) * h.x + static_cast<double>(h.y) * h.y;
+      const double u0 = fabs(static_cast<double>(h.x) * w.x), u1 = fabs(static_cast<double>(h.y) * w.y);
+      a = isfinite(u0) && isfinite(u1) ? fmax(a, fmax(u0, u1)) : CUDART_INF;
+    }
+  }
+  const auto reduce = [&] {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      a = fmax(a, __shfl_xor_sync(0xffffffffu, a, o));
+    }
+  };
+  reduce();
+  if (nw > 1) {
+    if (lane == 0) {
+      s_far[0][warp] = ss;
+      s_far[1][warp] = a;
+    }
+    __syncthreads();
+    ss = lane < nw ? s_far[0][lane] : 0.;
+    a = lane < nw ? s_far[1][lane] : 0.;
+    reduce();
+  }
+  const bool bad = isinf(a);
+  const double rstd = 1. / sqrt(ss / p.K + p.eps);
+  if (p.codes && threadIdx.x == 0) p.scale[m] = bad ? CUDART_NAN_F : static_cast<float>(a * rstd / 127.);
+  for (int c = threadIdx.x; c < nv; c += blockDim.x) {
+    uint32_t hw[4], ww[4];
+    load(c, hw, ww);
+    uint32_t o[4];
+    uint32_t out[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 h = bf16x2_to_f32x2(hw[i]), w = bf16x2_to_f32x2(ww[i]);
+      const double u0 = static_cast<double>(h.x) * w.x, u1 = static_cast<double>(h.y) * w.y;
+      o[i] = pack_bf16x2(static_cast<float>(u0 * rstd), static_cast<float>(u1 * rstd));
+      if (!bad && a > 0.) {
+        const uint32_t c0 = __double2int_rn(127. * u0 / a) & 255, c1 = __double2int_rn(127. * u1 / a) & 255;
+        out[i >> 1] |= (c0 | c1 << 8) << (i & 1) * 16;
+      }
+    }
+    if (p.y) reinterpret_cast<uint4*>(p.y + row)[c] = make_uint4(o[0], o[1], o[2], o[3]);
+    if (p.codes) reinterpret_cast<uint2*>(p.codes + row)[c] = make_uint2(out[0], out[1]);
+  }
+}
+
 // One row per blockIdx.x and threadIdx.y: kC chunks of eight values for each
 // of blockDim.x threads (a multiple of 32; one warp where blockDim.y > 1).
 // kNorm: the norm, else the quantisation alone.
 //
 // kKeep: a norm's u stays in registers between the maximum and the codes (up
-// to four chunks and 256 threads; beyond, that would cost the second block on
-// an SM, so h stays, packed, and the products are taken once more: 4096 x
-// 16384 with residual 71 us, 90 with u kept).
+// to 8192 values; beyond, that would cost the second block on an SM, so h stays, packed, and the products are taken once more: 4096 x
+// 16384 with residual 69 us, 90 with u kept).
 //
 // One or two chunks serve batches of few rows, where registers are free and
 // loads in flight are not: the second bound lets the compiler use 64 (1000 x
 // 4096 with residual 8.0 -> 7.4 us).
 template <int kC, bool kNorm, bool kKeep>
 __global__ void __launch_bounds__(rows_max_threads(kC, kKeep), kC <= 2 ? 1 : 0) ll_rows_i8_kernel(const RowsParams p) {
-  __shared__ __align__(16) float s_sum[2][32];
+  __shared__ __align__(16) float s_sum[32];
   __shared__ __align__(16) uint32_t s_max[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nw = blockDim.x >> 5;
@@ -121,7 +207,7 @@ __global__ void __launch_bounds__(rows_max_threads(kC, kKeep), kC <= 2 ? 1 : 0) 
   const auto gain = [&](int c) {
     return c < nv ? reinterpret_cast<const uint4*>(p.w)[c] : make_uint4(kOnes, kOnes, kOnes, kOnes);
   };
-  constexpr bool kAhead = kC <= 4;  // the gains' loads go out with x's
+  constexpr bool kAhead = kC <= 4 || kKeep;  // the gains' loads go out with x's
   uint4 wv[kAhead ? kC : 1];
   if (kNorm && kAhead && p.w) {
 #pragma unroll
@@ -154,7 +240,7 @@ __global__ void __launch_bounds__(rows_max_threads(kC, kKeep), kC <= 2 ? 1 : 0) 
         const uint4 wj = kAhead ? wv[kAhead ? j : 0] : gain(c);
         const uint32_t ww[4] = {wj.x, wj.y, wj.z, wj.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) uj[i] = mul2(uj[i], bf16x2_to_f32x2(ww[i]));
+        for (int i = 0; i < 4; ++i) uj[i] = mul_bf16x2(hw[i], ww[i]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -185,61 +271,40 @@ __global__ void __launch_bounds__(rows_max_threads(kC, kKeep), kC <= 2 ? 1 : 0) 
   if (nw > 1) {
     if (lane == 0) {
       s_max[warp] = mx;
-      s_sum[0][warp] = ss;
+      s_sum[warp] = ss;
     }
     __syncthreads();
-    if (nw <= 4) {
+    if (nw <= 8) {  // few enough to add up without shuffles (16384 x 8192 with residual 134.9 -> 134.4 us, 2048 x 8192 20.4 -> 19.8)
       const uint4 m4 = *reinterpret_cast<const uint4*>(s_max);
-      const float4 t4 = *reinterpret_cast<const float4*>(s_sum[0]);
+      const float4 t4 = *reinterpret_cast<const float4*>(s_sum);
       mx = max(m4.x, m4.y);
       ss = t4.x + t4.y;
-      if (nw > 2) {
-        mx = max(mx, m4.z);
-        ss += t4.z;
-      }
-      if (nw > 3) {
-        mx = max(mx, m4.w);
-        ss += t4.w;
+      if (nw > 2) mx = max(mx, m4.z), ss += t4.z;
+      if (nw > 3) mx = max(mx, m4.w), ss += t4.w;
+      if (nw > 4) {
+        const uint4 m5 = reinterpret_cast<const uint4*>(s_max)[1];
+        const float4 t5 = reinterpret_cast<const float4*>(s_sum)[1];
+        mx = max(mx, m5.x), ss += t5.x;
+        if (nw > 5) mx = max(mx, m5.y), ss += t5.y;
+        if (nw > 6) mx = max(mx, m5.z), ss += t5.z;
+        if (nw > 7) mx = max(mx, m5.w), ss += t5.w;
       }
     } else {
       mx = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[lane] : 0u);
-      if (kNorm) ss = warp_sum(lane < nw ? s_sum[0][lane] : 0.f);
+      if (kNorm) ss = warp_sum(lane < nw ? s_sum[lane] : 0.f);
     }
   }
   float a = __uint_as_float(mx), rstd = 1.f;
-  const bool bad = mx >= 0x7F800000u;
+  const bool bad = !kNorm && mx >= 0x7F800000u;
   if (kNorm) {
+    if (mx >= 0x7F800000u || isinf(ss) || (p.w && a < 0x1p-100f)) return norm_row_far(p, m);  // alike in all threads of the row
     if (p.y || threadIdx.x == 0) rstd = 1.f / sqrtf(fmaf(ss, p.inv_k, p.eps));
-    if (isinf(ss) && !bad) {
-      // Finite values whose squares overflow: the squares of h * 2^-64,
-      // beside which eps does not count.  h comes from memory once more: as
-      // this thread stored it, or from inputs that nothing has written.
-      float s2 = 0.f;
-      for (int c = threadIdx.x; c < nv; c += blockDim.x) {
-        uint4 v = reinterpret_cast<const uint4*>((p.h ? p.h : p.x) + row)[c];
-        if (p.residual && !p.h) {
-          const uint4 r = reinterpret_cast<const uint4*>(p.residual + row)[c];
-          v = make_uint4(add_bf16x2(v.x, r.x), add_bf16x2(v.y, r.y), add_bf16x2(v.z, r.z), add_bf16x2(v.w, r.w));
-        }
-        const uint32_t hw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 t = bf16x2_to_f32x2(hw[i]);
-          s2 = fmaf(t.x * 0x1p-64f, t.x * 0x1p-64f, s2);
-          s2 = fmaf(t.y * 0x1p-64f, t.y * 0x1p-64f, s2);
-        }
-      }
-      s2 = warp_sum(s2);
-      if (nw > 1) {
-        if (lane == 0) s_sum[1][warp] = s2;
-        __syncthreads();
-        s2 = warp_sum(lane < nw ? s_sum[1][lane] : 0.f);
-      }
-      rstd = 0x1p-64f / sqrtf(s2 * p.inv_k);
-    }
   }
-  if (p.codes && threadIdx.x == 0)
-    p.scale[m] = bad ? __int_as_float(0x7FC00000) : (kNorm ? a * rstd : a) / 127.f;
+  if (p.codes && threadIdx.x == 0) {
+    const bool big = a > 1.f;  // then a * rstd may overflow where the scale does not, else a / 127 underflow
+    const float t = (big ? a : a * rstd) / 127.f;
+    p.scale[m] = bad ? CUDART_NAN_F : (big ? t * rstd : t);
+  }
   // Rows far from 1 are scaled by a power of two, so that 1 / a, 127 u and
   // the corrections stay finite and normal.
   const float pre = a > 0x1p100f ? 0x1p-60f : (a < 0x1p-60f ? 0x1p80f : 1.f);
@@ -258,13 +323,14 @@ __global__ void __launch_bounds__(rows_max_threads(kC, kKeep), kC <= 2 ? 1 : 0) 
       for (int i = 0; i < 4; ++i) v[i] = u[j][i];
     } else {
       const uint32_t hw[4] = {hv[j].x, hv[j].y, hv[j].z, hv[j].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = bf16x2_to_f32x2(hw[i]);
       if (kNorm && p.w) {
         const uint4 wj = gain(c);
         const uint32_t ww[4] = {wj.x, wj.y, wj.z, wj.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], bf16x2_to_f32x2(ww[i]));
+        for (int i = 0; i < 4; ++i) v[i] = mul_bf16x2(hw[i], ww[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = bf16x2_to_f32x2(hw[i]);
       }
     }
     if (kNorm) {

@@ -106,6 +106,37 @@ def test_rows_of_every_magnitude(K):
     _check_quant(x)
 
 
+@pytest.mark.parametrize("K", [16, 512, 4096, 16400])
+def test_gains_of_every_magnitude(K):
+    """Products that leave binary32 in rows that do not."""
+    x = _special_rows(K)
+    one = 1 + 0.2 * _rows(1, K, 42, 0.0)[0].float()
+    for e in (-133, -120, -60, 60, 110):
+        w = (one * 2.0 ** e).to(BF16)
+        _check_norm(x, None, w)
+        _check_norm(x, torch.zeros_like(x), w, eps=1e-30)
+    w = (one.clamp(-1.9, 1.9) * 2.0 ** 127).to(BF16)  # y overflows, the scales do not
+    assert torch.isfinite(i8ref.rmsnorm(x, None, w, 1e-6)[3].float()).all()
+    _check_norm(x, None, w, y=False)
+    w[::2] *= 2.0 ** -126
+    w[1::4] = 0.0
+    _check_norm(x, x, w, y=False)
+
+
+@pytest.mark.parametrize("n,K", [(350, 4096), (345, 4240), (180, 8176), (176, 8192)])
+def test_many_long_rows_without_a_residual(n, K):
+    """Each of n * 12 rows as the same row among twelve."""
+    x = torch.cat([_special_rows(K)[1:], _rows(1, K, 40)])
+    w = (1 + 0.2 * _rows(1, K, 41, 0.0)[0].float()).to(BF16)
+    _, y, codes, scale = (t if t is None else t.view(n, 12, *t.shape[1:]) for t in _norm(x.repeat(n, 1), None, w))
+    _, ry, rc, rs = i8ref.rmsnorm(x, None, w, 1e-6)
+    i8ref.check_y(y[0], ry, i8ref.RSTD_TOL * ry.abs(), "y")
+    i8ref.check_scale(scale[0], rs, "scale")
+    assert torch.equal(codes[0], rc)
+    for t in (y, codes, scale):
+        assert torch.equal(t, t[:1].expand_as(t))
+
+
 @pytest.mark.parametrize("K", [16, 4096])
 def test_rows_with_nan_or_infinity_are_marked(K):
     x = _rows(6, K, 12)
