@@ -72,13 +72,15 @@ int launch_rows_i8(const llk::RowsParams& p, bool norm, int sms, cudaStream_t st
   // Norm with residual, us with 1 / 2 / 4 chunks: 100 x 8192 2.8 / 3.2 / 3.2,
   // 400 x 4096 5.0 / 3.9 / 4.2, 3630 x 4096 29.2 / 19.9 / 18.0, 16384 x 4096
   // 118 / 78 / 69.  Eight where four would need more than 1024 threads.
-  // Without a residual there is half as much to load beside the same work, and
-  // the reductions count: long rows take eight chunks by half the warps (us
-  // with 4 / 8: 1400 x 8192 11.4 / 11.1, 6000 x 8192 35.5 / 32.5, 16384 x 8192
+  // Many long rows whose norm's u fits 256 threads by eight chunks take those
+  // (us with 4 / 8: 4000 x 16384 68.8 / 68.7 and 47.5 / 42.7 without residual,
+  // 4000 x 12288 56.0 / 54.2 and 41.4 / 39.1; but 400 x 16384 10.7 / 11.0), and
+  // shorter ones without a residual: half as much to load beside the same
+  // work, and half the warps to join (1400 x 8192 11.4 / 11.1, 16384 x 8192
   // 89.8 / 80.7, 5000 x 6144 23.0 / 22.5; but 16384 x 4096 41.0 / 42.3, and
-  // with a residual 16384 x 8192 134 / 137).
+  // with residual 16384 x 8192 134 / 137).
   int c = p.M <= 2 * sms ? 1 : (p.M <= 8 * sms && nv <= 512 ? 2 : 4);
-  if (norm && !p.residual && c == 4 && p.M > 8 * sms && nv > 640 && nv <= 1024) c = 8;
+  if (norm && c == 4 && p.M > 8 * sms && nv <= 2048 && nv > (p.residual ? 1024 : 640)) c = 8;
   while (c < 8 && nv > 1024 * c) c *= 2;
   while (c > 1 && nv <= 16 * c) c /= 2;
   const int threads = ((nv + c - 1) / c + 31) / 32 * 32;

@@ -48,9 +48,9 @@ struct RowsParams {
 
 constexpr float kRound = 12582912.f;  // 1.5 * 2^23
 constexpr int kRowsMaxK = 1024 * 8 * 8;  // 1024 threads with 8 chunks of 8 values each
-// Threads per row that a kernel may have: 1024, or as many as 8192 values need
-// for four and eight chunks per thread with u kept.
-constexpr int rows_max_threads(int c, bool keep) { return c >= 4 && keep ? 1024 / c : 1024; }
+// Threads per row that a kernel may have: 1024, or 256 for four and eight
+// chunks per thread with u kept.
+constexpr int rows_max_threads(int c, bool keep) { return c >= 4 && keep ? 256 : 1024; }
 
 // The two bf16 of a word.
 __device__ __forceinline__ float2 bf16x2_to_f32x2(uint32_t v) {
@@ -177,9 +177,11 @@ __device__ __forceinline__ void norm_row_far(const RowsParams& p, int m) {
 // of blockDim.x threads (a multiple of 32; one warp where blockDim.y > 1).
 // kNorm: the norm, else the quantisation alone.
 //
-// kKeep: a norm's u stays in registers between the maximum and the codes (up
-// to 8192 values; beyond, that would cost the second block on an SM, so h stays, packed, and the products are taken once more: 4096 x
-// 16384 with residual 69 us, 90 with u kept).
+// kKeep: a norm's u stays in registers between the maximum and the codes, in
+// blocks of up to 256 threads.  Beyond, that would cost the second block on an
+// SM, so h stays, packed, and the products are taken once more (4000 x 16384
+// with residual 68.8 us by 512 threads, 90 with u kept; by 256 68.7, without
+// residual 47.5 and 42.7).
 //
 // One or two chunks serve batches of few rows, where registers are free and
 // loads in flight are not: the second bound lets the compiler use 64 (1000 x

@@ -123,18 +123,20 @@ def test_gains_of_every_magnitude(K):
     _check_norm(x, x, w, y=False)
 
 
-@pytest.mark.parametrize("n,K", [(350, 4096), (345, 4240), (180, 8176), (176, 8192)])
-def test_many_long_rows_without_a_residual(n, K):
+@pytest.mark.parametrize("n,K", [(350, 4096), (345, 4240), (180, 8176), (176, 8192), (110, 12304), (100, 16384)])
+def test_many_long_rows(n, K):
     """Each of n * 12 rows as the same row among twelve."""
     x = torch.cat([_special_rows(K)[1:], _rows(1, K, 40)])
     w = (1 + 0.2 * _rows(1, K, 41, 0.0)[0].float()).to(BF16)
-    _, y, codes, scale = (t if t is None else t.view(n, 12, *t.shape[1:]) for t in _norm(x.repeat(n, 1), None, w))
     _, ry, rc, rs = i8ref.rmsnorm(x, None, w, 1e-6)
-    i8ref.check_y(y[0], ry, i8ref.RSTD_TOL * ry.abs(), "y")
-    i8ref.check_scale(scale[0], rs, "scale")
-    assert torch.equal(codes[0], rc)
-    for t in (y, codes, scale):
-        assert torch.equal(t, t[:1].expand_as(t))
+    for r in (None, torch.zeros_like(x)):
+        xs, rs_ = x.repeat(n, 1), None if r is None else r.repeat(n, 1)
+        _, y, codes, scale = (t if t is None else t.view(n, 12, *t.shape[1:]) for t in _norm(xs, rs_, w))
+        i8ref.check_y(y[0], ry, i8ref.RSTD_TOL * ry.abs(), "y")
+        i8ref.check_scale(scale[0], rs, "scale")
+        assert torch.equal(codes[0], rc)
+        for t in (y, codes, scale):
+            assert torch.equal(t, t[:1].expand_as(t))
 
 
 @pytest.mark.parametrize("K", [16, 4096])
