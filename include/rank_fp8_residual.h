@@ -415,8 +415,8 @@ typedef struct ll_i8_layer *ll_i8_handle;
 /* Create a layer of N output and K input features on the current device.
  * N >= 1 and N % 8 == 0.  Device memory for the weight is allocated here.
  * Returns NULL on error (see ll_last_error()): LL_ERR_INVALID_ARG for bad
- * sizes, LL_ERR_UNSUPPORTED for K > 131056 (the int32 sum) or a GPU other
- * than sm_100, LL_ERR_OOM / LL_ERR_CUDA. */
+ * sizes, LL_ERR_UNSUPPORTED for K > 131056 (the int32 sum), N > 2^31 - 512
+ * or a GPU other than sm_100, LL_ERR_OOM / LL_ERR_CUDA. */
 ll_i8_handle ll_i8_create(int N, int K);
 
 /* Copy the weight into handle-owned device memory (synchronises the device;
@@ -432,7 +432,7 @@ int ll_i8_set_epilogue(ll_i8_handle h, int epilogue);
 /* y = forward(codes, scale) for M tokens: codes int8 [M, K] and y bf16
  * [M, N] 16-byte aligned, scale fp32 [M]; y must not overlap the inputs.
  * A NaN scale gives a row of NaN.  M == 0 is a no-op.  LL_ERR_NOT_READY
- * before ll_i8_set_weights. */
+ * before ll_i8_set_weights, LL_ERR_UNSUPPORTED for M > 2^31 - 512. */
 int ll_i8_forward(ll_i8_handle h, const void *codes, const float *scale, void *y, int M, void *stream);
 
 /* What a forward of M tokens through an (N, K) int8 layer runs on a GPU with

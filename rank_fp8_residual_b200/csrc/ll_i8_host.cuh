@@ -90,7 +90,7 @@ int launch_rows_i8(const llk::RowsParams& p, bool norm, int sms, cudaStream_t st
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((p.M + rows - 1) / rows);
+  cfg.gridDim = dim3((static_cast<unsigned>(p.M) + rows - 1) / rows);
   cfg.blockDim = dim3(threads, rows);
   cfg.stream = st;
   cfg.attrs = attr;
@@ -158,6 +158,7 @@ bool make_weight_maps(ll_i8_layer* h) {
 }
 const CUtensorMap& weight_map(const ll_i8_layer* h, int rows) { return h->tm_w[(rows - 32) / 16]; }
 
+constexpr int kI8MaxRows = 0x7FFFFFFF - 511;  // of either operand: a tile's rows behind the last still count in an int
 constexpr int kI8StreamMaxM = 256;  // the MMA's N
 
 // What a forward of M tokens runs, and the model's cycles.  The model's rates
@@ -372,7 +373,7 @@ ll_i8_handle ll_i8_create(int N, int K) {
     fail(LL_ERR_INVALID_ARG);
     return nullptr;
   }
-  if (K > llk::kI8MaxK) {
+  if (K > llk::kI8MaxK || N > kI8MaxRows) {
     fail(LL_ERR_UNSUPPORTED);
     return nullptr;
   }
@@ -464,6 +465,7 @@ int ll_i8_forward(ll_i8_handle h, const void* codes, const float* scale, void* y
   g_last_error = LL_OK;
   if (!h || M < 0) return fail(LL_ERR_INVALID_ARG);
   if (!h->ready) return fail(LL_ERR_NOT_READY);
+  if (M > kI8MaxRows) return fail(LL_ERR_UNSUPPORTED);
   if (M == 0) return LL_OK;
   if (!codes || !scale || !y || !aligned(codes, 16) || !aligned(scale, 4) || !aligned(y, 16))
     return fail(LL_ERR_INVALID_ARG);
@@ -487,7 +489,7 @@ int ll_i8_forward(ll_i8_handle h, const void* codes, const float* scale, void* y
 int ll_i8_plan(int N, int K, int M, int num_sms, int* kernel, int* tile_features, int* tile_tokens, int* splits) {
   g_last_error = LL_OK;
   if (N < 1 || N % 8 != 0 || K < 16 || K % 16 != 0 || M < 1 || num_sms < 2) return fail(LL_ERR_INVALID_ARG);
-  if (K > llk::kI8MaxK) return fail(LL_ERR_UNSUPPORTED);
+  if (K > llk::kI8MaxK || N > kI8MaxRows || M > kI8MaxRows) return fail(LL_ERR_UNSUPPORTED);
   ll_i8_layer view;  // what the planning reads
   view.N = N;
   view.K = K;

@@ -106,7 +106,7 @@ __device__ __forceinline__ uint32_t pack_codes(float2 a, float2 b) {
 // as this thread stored it, or from inputs that nothing has written.  A row
 // of zeros under a gain comes here too (3630 x 4096 of nothing else 34 us,
 // ordinary rows 17).
-__device__ __forceinline__ void norm_row_far(const RowsParams& p, int m) {
+__device__ __forceinline__ void norm_row_far(const RowsParams& p, unsigned m) {
   __shared__ double s_far[2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5, nv = p.K >> 3;
   const size_t row = static_cast<size_t>(m) * p.K;
@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(rows_max_threads(kC, kKeep), kC <= 2 ? 1 : 0) 
   const int nv = p.K >> 3;
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int m = blockIdx.x * blockDim.y + threadIdx.y;
-  if (m >= p.M) return;  // a whole warp, and no barrier follows for rows of one warp
+  const unsigned m = blockIdx.x * blockDim.y + threadIdx.y;  // may pass 2^31 behind the last row
+  if (m >= static_cast<unsigned>(p.M)) return;  // a whole warp, and no barrier follows for rows of one warp
   const size_t row = static_cast<size_t>(m) * p.K;
   uint4 hv[kC], rv[kC];
 #pragma unroll

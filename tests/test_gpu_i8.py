@@ -496,6 +496,9 @@ def test_empty_batches():
     layer = _layer(*_product_inputs(1, 64, 24, 74)[2:])
     assert layer.forward(c, s).shape == (0, 24)
     assert layer.forward(c.view(0, 5, 64), s.view(0, 5)).shape == (0, 5, 24)
+    with pytest.raises(ll.LLError) as e:  # and the other end: refused before any address is looked at
+        ll.ll_i8_forward(layer.handle, None, None, None, 2 ** 31 - 511)
+    assert e.value.code == ll.LL_ERR_UNSUPPORTED
 
 
 def test_tensors_of_other_strides_are_refused():

@@ -59,6 +59,15 @@ def test_layer_reduction_limit():
     assert 131056 * 128 * 128 < 2 ** 31 <= 131072 * 128 * 128
 
 
+def test_limit_of_the_rows():
+    """A tile that starts at the last row still counts its rows in an int."""
+    assert _code(ll.ll_i8_create, 2 ** 31 - 504, 16) == ll.LL_ERR_UNSUPPORTED
+    assert _code(ll.ll_i8_plan, 2 ** 31 - 504, 16, 1, 148) == ll.LL_ERR_UNSUPPORTED
+    assert _code(ll.ll_i8_plan, 8, 16, 2 ** 31 - 511, 148) == ll.LL_ERR_UNSUPPORTED
+    assert ll.ll_i8_plan(8, 16, 2 ** 31 - 512, 148)[0] != ll.LL_I8_STREAM
+    assert ll.ll_i8_plan(2 ** 31 - 512, 16, 1, 148)[0] == ll.LL_I8_STREAM
+
+
 def test_null_layer_is_refused():
     for fn in (lambda: ll.ll_i8_forward(None, A, B, C, 4, 0), lambda: ll.ll_i8_set_weights(None, A, B),
                lambda: ll.ll_i8_set_epilogue(None, 0), lambda: ll.ll_i8_set_debug(None, False, 1)):
