@@ -356,8 +356,8 @@ struct I8StreamParams {
   Watch watch;
 };
 
-constexpr int kIsEpiWarps = 8;
-constexpr int kIsThreads = 32 * (2 + kIsEpiWarps);  // 0 TMA producer, 1 MMA issuer and TMEM allocator, 2-9 epilogue
+// Warps: 0 TMA producer, 1 MMA issuer and TMEM allocator, the rest epilogue.
+__host__ __device__ constexpr int is_threads(int epi_warps) { return 32 * (2 + epi_warps); }
 constexpr int kIsMaxStages = 12;
 constexpr int kIsMaxSplit = 8;
 // The small ring leaves room for a second CTA on the SM: the next kernel's,
@@ -378,8 +378,8 @@ __host__ __device__ constexpr int is_smem_bytes(int Mt, int ring) {
 // memory (a warp's lanes are 32 features of a token).  With one the int32 sums
 // go through shared memory ([token][feature]), and the CTAs of the cluster add
 // them over distributed shared memory, each for every splits-th token.
-template <int kAct>
-__global__ void __launch_bounds__(kIsThreads, 1) ll_i8_stream_kernel(const __grid_constant__ I8StreamParams p) {
+template <int kAct, int kEpiWarps>
+__global__ void __launch_bounds__(is_threads(kEpiWarps), 1) ll_i8_stream_kernel(const __grid_constant__ I8StreamParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = align1024(smem_raw);
   const int sb = is_stage_bytes(p.Mt), ns = p.stages;
@@ -462,18 +462,19 @@ __global__ void __launch_bounds__(kIsThreads, 1) ll_i8_stream_kernel(const __gri
     if (one) mbar_wait_drain(drain, 0, p.watch);
     __syncwarp();
   } else {
-    // TMEM lane = feature, column = token; two warps share a lane quadrant and
-    // take alternate blocks of 16 tokens.
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    // TMEM lane = feature, column = token; the warps of a lane quadrant take
+    // turns at blocks of 16 tokens.
+    constexpr int kTurn = 16 * kEpiWarps / 4;
+    const int q = warp & 3, turn = (warp - 2) >> 2;
     const int f = f0 + 32 * q + lane;
     const float4 s2 = f < p.N ? __ldg(p.sb + f / 2) : make_float4(0.f, 0.f, 0.f, 0.f);
     const float s = f & 1 ? s2.y : s2.x, b = f & 1 ? s2.w : s2.z;
     int* part = reinterpret_cast<int*>(ring) + 32 * q + lane;
     float sx[16];  // of the next block's tokens
-    if (p.splits == 1) i8_token_scales(sx, p.sx, 16 * half, p.M);
+    if (p.splits == 1) i8_token_scales(sx, p.sx, 16 * turn, p.M);
     if (__all_sync(0xffffffffu, mbar_wait(acc_full, 0, p.watch, kErrTimeoutEpilogue))) {
       tc_fence_after();
-      for (int c = 16 * half; c < p.Mt; c += 32) {
+      for (int c = 16 * turn; c < p.Mt; c += kTurn) {
         uint32_t v[16];
         tmem_ld16_wait(tbase + ((32u * q) << 16) + c, v);
         if (p.splits > 1) {
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(kIsThreads, 1) ll_i8_stream_kernel(const __gri
           for (int i = 0; i < 16; ++i) part[(c + i) * 128] = static_cast<int>(v[i]);
         } else {
           i8_store_tokens<kAct>(v, sx, c, p.M, p.N, f, s, b, p.y);
-          i8_token_scales(sx, p.sx, c + 32, p.M);
+          i8_token_scales(sx, p.sx, c + kTurn, p.M);
         }
       }
     } else {
@@ -502,7 +503,7 @@ __global__ void __launch_bounds__(kIsThreads, 1) ll_i8_stream_kernel(const __gri
   if (ok && f0 + c < p.N) {
     const float4 s0v = __ldg(p.sb + (f0 + c) / 2), s1v = __ldg(p.sb + (f0 + c) / 2 + 1);
     const uint32_t part = smem_u32(ring) + 4 * c;
-    for (int m = z + warp * p.splits; m < p.M; m += (kIsThreads / 32) * p.splits) {
+    for (int m = z + warp * p.splits; m < p.M; m += (2 + kEpiWarps) * p.splits) {
       const float sm = ld_ahead(p.sx + m);
       int4 v[kIsMaxSplit];
 #pragma unroll

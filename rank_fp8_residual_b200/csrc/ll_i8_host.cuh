@@ -108,9 +108,13 @@ I8Fn kernel_i8(int epilogue, bool swap) {
   if (epilogue == LL_EPILOGUE_GELU_TANH) return swap ? ll_i8_kernel<kActGelu, true> : ll_i8_kernel<kActGelu, false>;
   return swap ? ll_i8_kernel<kActNone, true> : ll_i8_kernel<kActNone, false>;
 }
-I8StreamFn kernel_i8_stream(int epilogue) {
-  return epilogue == LL_EPILOGUE_GELU_TANH ? llk::ll_i8_stream_kernel<llk::kActGelu>
-                                           : llk::ll_i8_stream_kernel<llk::kActNone>;
+template <int kEpiWarps>
+I8StreamFn kernel_i8_stream_as(int epilogue) {
+  return epilogue == LL_EPILOGUE_GELU_TANH ? llk::ll_i8_stream_kernel<llk::kActGelu, kEpiWarps>
+                                           : llk::ll_i8_stream_kernel<llk::kActNone, kEpiWarps>;
+}
+I8StreamFn kernel_i8_stream(int epilogue, int epi_warps) {
+  return epi_warps == 16 ? kernel_i8_stream_as<16>(epilogue) : kernel_i8_stream_as<8>(epilogue);
 }
 
 // Per device: the kernels' shared-memory limits, and how many clusters of
@@ -120,7 +124,9 @@ bool setup_i8(ll_i8_layer* h) {
   for (int e : {LL_EPILOGUE_NONE, LL_EPILOGUE_GELU_TANH})
     if (cudaFuncSetAttribute(kernel_i8(e, false), cudaFuncAttributeMaxDynamicSharedMemorySize, i8_smem_bytes()) != cudaSuccess ||
         cudaFuncSetAttribute(kernel_i8(e, true), cudaFuncAttributeMaxDynamicSharedMemorySize, i8_smem_bytes()) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel_i8_stream(e), cudaFuncAttributeMaxDynamicSharedMemorySize, kIsRingLarge + 1280) !=
+        cudaFuncSetAttribute(kernel_i8_stream(e, 8), cudaFuncAttributeMaxDynamicSharedMemorySize, kIsRingLarge + 1280) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(kernel_i8_stream(e, 16), cudaFuncAttributeMaxDynamicSharedMemorySize, kIsRingLarge + 1280) !=
             cudaSuccess)
       return false;
   for (int s = 2; s <= kIsMaxSplit; ++s) {
@@ -131,11 +137,11 @@ bool setup_i8(ll_i8_layer* h) {
     attr[0].val.clusterDim.y = static_cast<unsigned>(s);
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(h->num_sms, s);
-    cfg.blockDim = dim3(kIsThreads);
+    cfg.blockDim = dim3(is_threads(8));
     cfg.dynamicSmemBytes = kIsRingLarge + 1280;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&h->clusters[s], kernel_i8_stream(LL_EPILOGUE_NONE), &cfg) != cudaSuccess)
+    if (cudaOccupancyMaxActiveClusters(&h->clusters[s], kernel_i8_stream(LL_EPILOGUE_NONE, 8), &cfg) != cudaSuccess)
       return false;
   }
   h->clusters[1] = h->num_sms;
@@ -243,7 +249,11 @@ int launch_i8_stream(const ll_i8_layer* h, const I8Plan& plan, const void* codes
   p.splits = plan.splits;
   // At least four slots: a split's sums (512 bytes per token) go where the ring
   // was, and 4 (16384 + 128 Mt) >= 512 Mt.
-  const bool small = is_stages(p.Mt, kIsRingSmall) >= 4 && (p.Mt <= 32 || p.steps <= 16);
+  // The small one where the next kernel's start under this one's end counts for
+  // more than loads in flight (us small / large: 1 x 4096 -> 4096 4.95 / 5.44,
+  // 32 x 4096 -> 4096 5.70 / 6.03; 64 x 8192 -> 2048 7.4 / 7.0, 64 x 4096 ->
+  // 16384 15.3 / 13.8; with four K steps or fewer they fit it anyway).
+  const bool small = is_stages(p.Mt, kIsRingSmall) >= 4 && (p.Mt <= 32 || p.steps <= 4);
   const int ring = small ? kIsRingSmall : kIsRingLarge;
   p.stages = is_stages(p.Mt, ring);
   cudaLaunchConfig_t cfg = {};
@@ -254,13 +264,17 @@ int launch_i8_stream(const ll_i8_layer* h, const I8Plan& plan, const void* codes
   attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = static_cast<unsigned>(p.splits);
   attr[1].val.clusterDim.z = 1;
+  // Twice the epilogue warps where they store the outputs of more than 32
+  // tokens (64 x 4096 -> 16384 13.9 -> 13.6 us, 80 x 8192 -> 8192 15.8 -> 15.5);
+  // with a split they only move sums (128 x 8192 -> 2048 8.4 -> 8.7).
+  const int epi_warps = p.splits == 1 && p.Mt > 32 ? 16 : 8;
   cfg.gridDim = dim3((h->N + 127) / 128, p.splits);
-  cfg.blockDim = dim3(kIsThreads);
+  cfg.blockDim = dim3(is_threads(epi_warps));
   cfg.dynamicSmemBytes = is_smem_bytes(p.Mt, ring);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = p.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel_i8_stream(h->epilogue), p) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel_i8_stream(h->epilogue, epi_warps), p) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
 }
 
 int launch_i8(const ll_i8_layer* h, const I8Plan& plan, const void* codes, const float* scale, void* y, int M,
