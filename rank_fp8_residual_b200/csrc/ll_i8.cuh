@@ -54,9 +54,24 @@ __device__ __forceinline__ void i8_token_scales(float (&v)[16], const float* sx,
   }
 }
 
-// Outputs of one feature (this lane's; s, b its scale and bias) for the 16
-// tokens from m0 on, whose scales are sm: a warp's lanes are 32 neighbouring
-// features, 64 bytes of a token's row.
+// Outputs of one feature (this lane's; s, b its scale and bias) for 16 tokens
+// whose scales are sm, into a staging tile [token][32 features]: lanes of
+// neighbouring features swap halves, so that each writes one token's pair.
+template <int kAct>
+__device__ __forceinline__ void i8_stage_tokens(const uint32_t (&v)[16], const float (&sm)[16], float s, float b,
+                                                uint8_t* tile, int lane) {
+  uint32_t* d = reinterpret_cast<uint32_t*>(tile + (lane & 1) * 64) + lane / 2;
+  const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const uint32_t w =
+        i8_out2<kAct>(static_cast<int>(v[i]), static_cast<int>(v[i + 1]), s, make_float4(sm[i], sm[i + 1], b, b));
+    d[16 * i] = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), sel);
+  }
+}
+
+// The same for the 16 tokens from m0 on, straight to y (few tokens, where the
+// staging's round trip would show): 64 bytes of a token's row per warp.
 template <int kAct>
 __device__ __forceinline__ void i8_store_tokens(const uint32_t (&v)[16], const float (&sm)[16], int m0, int M, int N,
                                                 int f, float s, float b, uint16_t* __restrict__ y) {
@@ -79,11 +94,11 @@ __device__ __forceinline__ void i8_store_tokens(const uint32_t (&v)[16], const f
 // tokens, b the features; a thread of the epilogue owns a token, and the outputs
 // go through shared memory and TMA stores.  kSwap = true: a is the features, b
 // the tokens (batches whose tokens would fill tiles of 256 badly); a thread
-// owns a feature and stores it token by token.
+// owns a feature.
 struct I8Params {
   CUtensorMap tm_x;  // s8 xq [M, K]  box {128, rows}, 128B swizzle
   CUtensorMap tm_w;  // s8 weight panels [K / 128][N][128]  box {128, rows, 1}, 128B swizzle
-  CUtensorMap tm_y;  // bf16 y [M, N] box {32, 32}, 64B swizzle (kSwap = false)
+  CUtensorMap tm_y;  // bf16 y [M, N] box {32, 32}, 64B swizzle, or {32, 16} without (kSwap)
   const float* sx;       // [M]
   const float4* sb;      // [N rounded up / 2] (scale, scale, bias, bias) of two features
   uint16_t* y;           // [M, N] bf16 bits
@@ -154,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     fence_mbar_init();
     tma_prefetch_desc(&p.tm_x);
     tma_prefetch_desc(&p.tm_w);
-    if (!kSwap) tma_prefetch_desc(&p.tm_y);
+    tma_prefetch_desc(&p.tm_y);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -292,8 +307,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
         for (int c = 16 * half; c < w && b0 + c < p.M; c += 32) {
           uint32_t v[16];
           tmem_ld16_wait(acc + c, v);
-          i8_store_tokens<kAct>(v, sx, b0 + c, p.M, p.N, row, sm, bias, p.y);
+          if (lane == 0) tma_store_wait_read<1>();
+          __syncwarp();
+          uint8_t* st = stg + eb * (16 * 64);
+          i8_stage_tokens<kAct>(v, sx, sm, bias, st, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          store_2d_one(&p.tm_y, smem_u32(st), row0, b0 + c, row0 < p.N, lane == 0);
           if (c + 32 < w) i8_token_scales(sx, p.sx, b0 + c + 32, p.M);
+          eb ^= 1;
         }
       } else {
         for (int c = 32 * half; c < w; c += 64) {
@@ -327,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
           mbar_arrive_cluster(tempty_leader + 8u * buf);
       }
     }
-    if (!kSwap && lane == 0) tma_store_wait<0>();
+    if (lane == 0) tma_store_wait<0>();
   }
 
   tc_fence_before();
@@ -343,6 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 struct I8StreamParams {
   CUtensorMap tm_x;  // s8 xq [M, K] box {128, Mt},  128B swizzle
   CUtensorMap tm_w;  // s8 weight panels [K / 128][N][128] box {128, 128, 1}, 128B swizzle
+  CUtensorMap tm_y;  // bf16 y [M, N] box {32, 16} (16 epilogue warps)
   const float* sx;   // [M]
   const float4* sb;  // [N rounded up / 2] (scale, scale, bias, bias) of two features
   uint16_t* y;       // [M, N] bf16 bits
@@ -375,7 +398,8 @@ __host__ __device__ constexpr int is_smem_bytes(int Mt, int ring) {
 // One CTA (or a cluster that splits K) per tile of 128 features x all tokens:
 // the weight is read once from HBM, features on the MMA's M side, tokens on
 // its N side.  Without a split the outputs go straight from TMEM to global
-// memory (a warp's lanes are 32 features of a token).  With one the int32 sums
+// memory (a warp's lanes are 32 features of a token), or through staging tiles
+// and TMA stores by 16 epilogue warps, a launch for more than 32 tokens.  With one the int32 sums
 // go through shared memory ([token][feature]), and the CTAs of the cluster add
 // them over distributed shared memory, each for every splits-th token.
 template <int kAct, int kEpiWarps>
@@ -393,6 +417,8 @@ __global__ void __launch_bounds__(is_threads(kEpiWarps), 1) ll_i8_stream_kernel(
   const int f0 = blockIdx.x * 128;
   const int z = blockIdx.y;  // split of K = rank in the cluster
   const int s0 = z * p.steps;
+  constexpr bool kStaged = kEpiWarps > 8;  // outputs go through staging tiles; no split then
+  const bool split = !kStaged && p.splits > 1;
   const int n = min((p.K + 127) / 128 - s0, p.steps);  // K steps of this CTA (>= 1 by the plan)
 
   if (threadIdx.x == 0) {
@@ -471,20 +497,30 @@ __global__ void __launch_bounds__(is_threads(kEpiWarps), 1) ll_i8_stream_kernel(
     const float s = f & 1 ? s2.y : s2.x, b = f & 1 ? s2.w : s2.z;
     int* part = reinterpret_cast<int*>(ring) + 32 * q + lane;
     float sx[16];  // of the next block's tokens
-    if (p.splits == 1) i8_token_scales(sx, p.sx, 16 * turn, p.M);
+    if (!split) i8_token_scales(sx, p.sx, 16 * turn, p.M);
     if (__all_sync(0xffffffffu, mbar_wait(acc_full, 0, p.watch, kErrTimeoutEpilogue))) {
       tc_fence_after();
       for (int c = 16 * turn; c < p.Mt; c += kTurn) {
         uint32_t v[16];
         tmem_ld16_wait(tbase + ((32u * q) << 16) + c, v);
-        if (p.splits > 1) {
+        if (split) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) part[(c + i) * 128] = static_cast<int>(v[i]);
-        } else {
+        } else if (!kStaged) {
           i8_store_tokens<kAct>(v, sx, c, p.M, p.N, f, s, b, p.y);
+          i8_token_scales(sx, p.sx, c + kTurn, p.M);
+        } else {
+          if (lane == 0) tma_store_wait_read<1>();
+          __syncwarp();
+          uint8_t* st = ring + (2 * (warp - 2) + ((c / kTurn) & 1)) * (16 * 64);  // the MMAs are done with the ring
+          i8_stage_tokens<kAct>(v, sx, s, b, st, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          store_2d_one(&p.tm_y, smem_u32(st), f0 + 32 * q, c, f0 + 32 * q < p.N && c < p.M, lane == 0);
           i8_token_scales(sx, p.sx, c + kTurn, p.M);
         }
       }
+      if (kStaged && lane == 0) tma_store_wait<0>();
     } else {
       ok = false;
     }
@@ -495,7 +531,7 @@ __global__ void __launch_bounds__(is_threads(kEpiWarps), 1) ll_i8_stream_kernel(
     tc_fence_after();
     tmem_dealloc(tbase, p.tmem_cols);
   }
-  if (p.splits == 1) return;
+  if (!split) return;
   // After a timeout the sums are incomplete; the CTA still takes part in both
   // cluster barriers.
   cluster_sync();

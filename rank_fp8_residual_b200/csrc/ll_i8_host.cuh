@@ -268,6 +268,9 @@ int launch_i8_stream(const ll_i8_layer* h, const I8Plan& plan, const void* codes
   // tokens (64 x 4096 -> 16384 13.9 -> 13.6 us, 80 x 8192 -> 8192 15.8 -> 15.5);
   // with a split they only move sums (128 x 8192 -> 2048 8.4 -> 8.7).
   const int epi_warps = p.splits == 1 && p.Mt > 32 ? 16 : 8;
+  if (epi_warps == 16 &&
+      !make_map(&p.tm_y, y, kBF16, M, h->N, 2ull * h->N, 32, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return LL_ERR_CUDA;
   cfg.gridDim = dim3((h->N + 127) / 128, p.splits);
   cfg.blockDim = dim3(is_threads(epi_warps));
   cfg.dynamicSmemBytes = is_smem_bytes(p.Mt, ring);
@@ -286,7 +289,8 @@ int launch_i8(const ll_i8_layer* h, const I8Plan& plan, const void* codes, const
   p.w = plan.w;
   if (!make_map(&p.tm_x, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, M, h->K, h->K, 128, plan.swap ? p.w / 2 : 128,
                 CU_TENSOR_MAP_SWIZZLE_128B) ||
-      (!plan.swap && !make_map(&p.tm_y, y, kBF16, M, h->N, 2ull * h->N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)))
+      !make_map(&p.tm_y, y, kBF16, M, h->N, 2ull * h->N, 32, plan.swap ? 16 : 32,
+                plan.swap ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B))
     return LL_ERR_CUDA;
   p.tm_w = weight_map(h, plan.swap ? 128 : p.w / 2);
   p.sx = scale;
