@@ -175,7 +175,9 @@ constexpr int kI8StreamMaxM = 256;  // the MMA's N
 //   products of a 256 x w step take 2.2 w cycles (2 w alone);
 //   start and end cost 5,000 (pair) or 5,560 (streaming), and the last tile's
 //   epilogue 4,500 per 256 columns (11,000 with kSwap's stores token by token)
-//   or 42 per token (streaming).
+//   or 42 per token (streaming), 5 % of which starts under the kernel before;
+//   a streaming launch with 16 epilogue warps all but hides them (60 per token
+//   above 25).
 struct I8Plan {
   bool stream;
   int splits, steps;  // streaming: CTAs per tile and K steps of each
@@ -204,6 +206,22 @@ I8Plan i8_plan_pair(const ll_i8_layer* h, int M) {
   return best;
 }
 
+// Twice the epilogue warps, and outputs by staging tiles and TMA stores, where
+// a launch without a split has more than 32 tokens (64 x 4096 -> 16384 13.9 ->
+// 13.15 us, 80 x 8192 -> 8192 15.8 -> 15.7); with a split the warps only move
+// sums (128 x 8192 -> 2048 8.4 -> 8.7).
+bool i8_staged(int splits, int Mt) { return splits == 1 && Mt > 32; }
+
+// The small ring where the next kernel's start under this one's end counts for
+// more than loads in flight (us small / large: 1 x 4096 -> 4096 4.95 / 5.44, 32 x
+// 4096 -> 4096 5.70 / 6.03; 64 x 8192 -> 2048 7.4 / 7.0, 64 x 4096 -> 16384 15.3 /
+// 13.8; with four K steps or fewer they fit it anyway).  At least four slots: a
+// split's sums (512 bytes per token) go where the ring was, and 4 (16384 +
+// 128 Mt) >= 512 Mt.
+bool is_small_ring(int steps, int Mt) {
+  return llk::is_stages(Mt, llk::kIsRingSmall) >= 4 && (Mt <= 32 || steps <= 4);
+}
+
 I8Plan i8_plan_stream(const ll_i8_layer* h, int M) {
   const int tiles = (h->N + 127) / 128, steps = (h->K + 127) / 128, Mt = (M + 15) / 16 * 16;
   // As many CTAs as fit at once share the K steps of a tile.
@@ -214,18 +232,27 @@ I8Plan i8_plan_stream(const ll_i8_layer* h, int M) {
   p.steps = (steps + s - 1) / s;
   p.splits = (steps + p.steps - 1) / p.steps;
   const double waves = std::ceil(static_cast<double>(tiles) * p.splits / h->num_sms);
-  p.cycles = 5560.0 + std::max(waves * p.steps * (16384.0 + 128.0 * Mt) / 66.0, i8_weight_cycles(h)) + 42.0 * M;
+  const double step = (16384.0 + 128.0 * Mt) / 66.0, loop = std::max(waves * p.steps * step, i8_weight_cycles(h));
+  if (!i8_staged(p.splits, Mt))
+    p.cycles = 0.95 * (loop + 5560.0 + 42.0 * M);
+  else if (waves == 1)
+    p.cycles = loop + 60.0 * M - 1500.0;
+  else  // one CTA per SM: its rounds follow one another (us, streaming / pair: 40 x 4096 -> 19000 20.7 / 18.6, 64 x 1024 ->
+        // 28000 10.2 / 12.9, 64 x 128 -> 19000 3.4 / 6.4)
+    p.cycles = 0.95 * std::max(waves * (p.steps * step + std::min(5800.0, 2000.0 + 450.0 * p.steps)),
+                               i8_weight_cycles(h));
   return p;
 }
 
 // Measured (us, streaming / pair): 1024 -> 1024: M = 32 4.1 / 4.6, 128 6.0 /
-// 4.7; 4096 -> 4096: 64 7.0 / 9.8, 256 11.3 / 10.2; 4096 -> 16384: 64 14.3 /
-// 14.9, 256 24.5 / 18.4; 8192 -> 2048: 256 12.8 / 14.6.
+// 4.7; 4096 -> 4096: 64 7.0 / 9.8, 256 11.4 / 9.6; 4096 -> 16384: 96 14.0 /
+// 16.2, 160 16.3 / 17.6, 200 18.6 / 17.5, 256 19.7 / 17.9; 1024 -> 16384: 128
+// 5.9 / 7.8; 8192 -> 8192: 100 16.4 / 16.2; 8192 -> 2048: 256 12.8 / 14.6.
 I8Plan i8_plan(const ll_i8_layer* h, int M) {
   const I8Plan pair = i8_plan_pair(h, M);
   if (M > kI8StreamMaxM) return pair;
   const I8Plan stream = i8_plan_stream(h, M);
-  return pair.cycles < 0.95 * stream.cycles ? pair : stream;
+  return pair.cycles < stream.cycles ? pair : stream;
 }
 
 int launch_i8_stream(const ll_i8_layer* h, const I8Plan& plan, const void* codes, const float* scale, void* y, int M,
@@ -247,14 +274,7 @@ int launch_i8_stream(const ll_i8_layer* h, const I8Plan& plan, const void* codes
   p.watch = Watch{h->status, h->timeout_ns};
   p.steps = plan.steps;
   p.splits = plan.splits;
-  // At least four slots: a split's sums (512 bytes per token) go where the ring
-  // was, and 4 (16384 + 128 Mt) >= 512 Mt.
-  // The small one where the next kernel's start under this one's end counts for
-  // more than loads in flight (us small / large: 1 x 4096 -> 4096 4.95 / 5.44,
-  // 32 x 4096 -> 4096 5.70 / 6.03; 64 x 8192 -> 2048 7.4 / 7.0, 64 x 4096 ->
-  // 16384 15.3 / 13.8; with four K steps or fewer they fit it anyway).
-  const bool small = is_stages(p.Mt, kIsRingSmall) >= 4 && (p.Mt <= 32 || p.steps <= 4);
-  const int ring = small ? kIsRingSmall : kIsRingLarge;
+  const int ring = is_small_ring(p.steps, p.Mt) ? kIsRingSmall : kIsRingLarge;
   p.stages = is_stages(p.Mt, ring);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -264,10 +284,7 @@ int launch_i8_stream(const ll_i8_layer* h, const I8Plan& plan, const void* codes
   attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = static_cast<unsigned>(p.splits);
   attr[1].val.clusterDim.z = 1;
-  // Twice the epilogue warps where they store the outputs of more than 32
-  // tokens (64 x 4096 -> 16384 13.9 -> 13.6 us, 80 x 8192 -> 8192 15.8 -> 15.5);
-  // with a split they only move sums (128 x 8192 -> 2048 8.4 -> 8.7).
-  const int epi_warps = p.splits == 1 && p.Mt > 32 ? 16 : 8;
+  const int epi_warps = i8_staged(p.splits, p.Mt) ? 16 : 8;
   if (epi_warps == 16 &&
       !make_map(&p.tm_y, y, kBF16, M, h->N, 2ull * h->N, 32, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
     return LL_ERR_CUDA;

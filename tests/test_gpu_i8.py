@@ -279,6 +279,7 @@ PRODUCT_SHAPES = [(1, 16, 8), (1, 4096, 1000), (2, 64, 136), (3, 2048, 2048), (4
                   (700, 336, 120), (1025, 512, 1536), (1300, 2048, 2048), (2500, 144, 4096),
                   # features on the pairs' long side, tokens in narrow tiles
                   (65, 2064, 16384), (96, 4096, 16392), (128, 4096, 16384), (257, 1024, 16392), (300, 4096, 16384),
+                  (80, 2048, 8192), (129, 2064, 8200), (257, 1040, 18944),
                   # streaming without a split of K, and one K step
                   (40, 4096, 16392), (7, 64, 2048), (200, 16, 8), (64, 128, 19000)]
 

@@ -14,7 +14,8 @@ S, P, W = ll.LL_I8_STREAM, ll.LL_I8_PAIR, ll.LL_I8_PAIR_SWAP
 @pytest.mark.parametrize("M,K,N,kernel", [
     (1, 4096, 16384, S), (64, 4096, 16384, S), (256, 4096, 16384, P), (300, 4096, 16384, W), (512, 4096, 16384, P),
     (64, 4096, 4096, S), (128, 4096, 4096, S), (256, 4096, 4096, P), (32, 1024, 1024, S), (128, 1024, 1024, P),
-    (256, 8192, 2048, S), (64, 2048, 2048, S), (3630, 2048, 8192, P), (16384, 4096, 16384, P)])
+    (96, 4096, 16384, S), (160, 4096, 16384, S), (200, 4096, 16384, P), (128, 1024, 16384, S), (128, 4096, 8192, W),
+    (40, 4096, 19000, W), (64, 128, 19000, S), (64, 1024, 28000, S), (100, 4096, 19000, P), (256, 8192, 2048, S), (64, 2048, 2048, S), (3630, 2048, 8192, P), (16384, 4096, 16384, P)])
 def test_measured_crossovers(M, K, N, kernel):
     assert ll.ll_i8_plan(N, K, M, 148)[0] == kernel
 
