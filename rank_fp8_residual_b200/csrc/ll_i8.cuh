@@ -28,15 +28,17 @@ namespace llk {
 
 constexpr int kI8MaxK = 131056;
 
-// Two outputs from their sums: first scaled by sm, then s = (scale, scale, bias,
-// bias).  The sum takes one scale after the other, as the formula's factors may
-// be far from 1 where their product with it is not.  GELU:
+// Two outputs from their sums: scaled by their tokens' scales sm, then s =
+// (scale, scale, bias, bias) of their features.  The sum takes one scale after
+// the other, as the formula's factors may be far from 1 where their product with
+// it is not, and the token's first in every kernel, so that a token's outputs
+// do not depend on the batch (and so the kernel) that it comes in.  GELU:
 // v / 2 (1 + tanh(z)) = v / (1 + exp(-2 z)), z = sqrt(2 / pi) (v + 0.044715 v^3);
 // exp(-2 z) as a power of two: -2 z log2(e) = v (-2.3022082 - 0.10294324 v^2).
 template <int kAct>
-__device__ __forceinline__ uint32_t i8_out2(int a0, int a1, float sm, const float4& s) {
-  float2 v = fma2(mul2(make_float2(static_cast<float>(a0), static_cast<float>(a1)), make_float2(sm, sm)),
-                  make_float2(s.x, s.y), make_float2(s.z, s.w));
+__device__ __forceinline__ uint32_t i8_out2(int a0, int a1, float2 sm, const float4& s) {
+  float2 v = fma2(mul2(make_float2(static_cast<float>(a0), static_cast<float>(a1)), sm), make_float2(s.x, s.y),
+                  make_float2(s.z, s.w));
   if constexpr (kAct == kActGelu) {
     const float2 t = mul2(v, fma2(mul2(v, v), make_float2(-0.10294324f, -0.10294324f),
                                   make_float2(-2.3022082f, -2.3022082f)));
@@ -62,10 +64,11 @@ __device__ __forceinline__ void i8_stage_tokens(const uint32_t (&v)[16], const f
                                                 uint8_t* tile, int lane) {
   uint32_t* d = reinterpret_cast<uint32_t*>(tile + (lane & 1) * 64) + lane / 2;
   const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
+  const float4 sb = make_float4(s, s, b, b);
 #pragma unroll
   for (int i = 0; i < 16; i += 2) {
     const uint32_t w =
-        i8_out2<kAct>(static_cast<int>(v[i]), static_cast<int>(v[i + 1]), s, make_float4(sm[i], sm[i + 1], b, b));
+        i8_out2<kAct>(static_cast<int>(v[i]), static_cast<int>(v[i + 1]), make_float2(sm[i], sm[i + 1]), sb);
     d[16 * i] = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), sel);
   }
 }
@@ -76,10 +79,11 @@ template <int kAct>
 __device__ __forceinline__ void i8_store_tokens(const uint32_t (&v)[16], const float (&sm)[16], int m0, int M, int N,
                                                 int f, float s, float b, uint16_t* __restrict__ y) {
   uint16_t* d = y + static_cast<size_t>(m0) * N + f;
+  const float4 sb = make_float4(s, s, b, b);
 #pragma unroll
   for (int i = 0; i < 16; i += 2) {
     const uint32_t w =
-        i8_out2<kAct>(static_cast<int>(v[i]), static_cast<int>(v[i + 1]), s, make_float4(sm[i], sm[i + 1], b, b));
+        i8_out2<kAct>(static_cast<int>(v[i]), static_cast<int>(v[i + 1]), make_float2(sm[i], sm[i + 1]), sb);
     if (f < N && m0 + i < M) d[static_cast<size_t>(i) * N] = static_cast<uint16_t>(w);
     if (f < N && m0 + i + 1 < M) d[static_cast<size_t>(i + 1) * N] = static_cast<uint16_t>(w >> 16);
   }
@@ -325,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
           uint32_t o[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            o[i] = i8_out2<kAct>(static_cast<int>(v[2 * i]), static_cast<int>(v[2 * i + 1]), sm, sb[i]);
+            o[i] = i8_out2<kAct>(static_cast<int>(v[2 * i]), static_cast<int>(v[2 * i + 1]), make_float2(sm, sm), sb[i]);
           if (c + 64 < w) load_sb(c + 64);
           if (lane == 0) tma_store_wait_read<1>();
           __syncwarp();
@@ -540,7 +544,8 @@ __global__ void __launch_bounds__(is_threads(kEpiWarps), 1) ll_i8_stream_kernel(
     const float4 s0v = __ldg(p.sb + (f0 + c) / 2), s1v = __ldg(p.sb + (f0 + c) / 2 + 1);
     const uint32_t part = smem_u32(ring) + 4 * c;
     for (int m = z + warp * p.splits; m < p.M; m += (2 + kEpiWarps) * p.splits) {
-      const float sm = ld_ahead(p.sx + m);
+      const float sx = ld_ahead(p.sx + m);
+      const float2 sm = make_float2(sx, sx);
       int4 v[kIsMaxSplit];
 #pragma unroll
       for (int r = 0; r < kIsMaxSplit; ++r)
