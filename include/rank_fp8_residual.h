@@ -409,7 +409,12 @@ int ll_quantize_i8(const void *x, int M, int K, void *codes, float *scale, void 
  *   y[m, n] = bf16(act(xs[m] * ws[n] * sum_k xq[m, k] wq[n, k] + bias[n]))
  *
  * xq, wq int8 codes ([M, K] and [N, K]; -128 is allowed), xs [M] and ws [N]
- * fp32, bias bf16.  The sum is exact (int32). */
+ * fp32, bias bf16.  The sum is exact (int32).  It is multiplied by xs[m] first
+ * and by ws[n] with the bias's addition then, each rounded to binary32, for every
+ * M: a token's outputs do not depend on the batch that it comes in.  |xs[m]| <
+ * 2^96 (the product with a sum then stays in binary32, and none is too small for
+ * it); ws[n] is any finite value.  A result beyond binary32 is infinite, and the
+ * GELU of minus infinity NaN. */
 typedef struct ll_i8_layer *ll_i8_handle;
 
 /* Create a layer of N output and K input features on the current device.

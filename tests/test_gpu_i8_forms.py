@@ -5,6 +5,7 @@ that they are planned so."""
 import pytest
 import torch
 
+import i8ref
 import rank_fp8_residual_b200 as ll
 from test_gpu_i8 import _forward, _layer, _product_inputs
 
@@ -44,3 +45,40 @@ def test_a_row_does_not_depend_on_its_batch(nk):
         n = min(n, want.shape[0])
         assert torch.equal(got[:n], want[:n]), f"{M} tokens: {int((got[:n] != want[:n]).sum())} outputs differ"
         want = got if got.shape[0] > want.shape[0] else want
+
+
+def _far_scales(M, N):
+    """Token scales up to the 2^96 that the layer takes, feature scales anywhere
+    in binary32."""
+    xe = torch.tensor([7.9e28, 1.0, 2.0 ** -149, 1e-30, -1e28, 2.0 ** -120, 1e-10, 7e28])
+    we = torch.tensor([1e33, 1e-30, 2.0 ** -140, 1e-38, 2.0 ** 120, -3.4e38, 1.0, 3e-45])
+    return xe[torch.arange(M) % 8], we[torch.arange(N) % 8]
+
+
+@pytest.mark.parametrize("nk,form,M", CASES)
+def test_scales_far_from_one_on_every_form(nk, form, M):
+    """Scales of features far from 1 meet sums that their tokens' scales have
+    brought back, or not: (sum, scale of the token, of the feature) = (1e6, 1e-30,
+    1e33) is 1e9 although the sum times 1e33 is beyond binary32.  Infinite where
+    the output is beyond bf16, the bias where the sum is zero."""
+    N, K = nk
+    g = torch.Generator().manual_seed(M)
+    xq = torch.randint(-127, 128, (M, K), generator=g, dtype=torch.int8)
+    xq[0] = 0
+    n = 64  # features, repeated: the reference needs no more
+    wq = torch.randint(-128, 128, (n, K), generator=g, dtype=torch.int8)
+    xs, ws = _far_scales(M, n)
+    assert xs.abs().max() < 2.0 ** 96 < 1.01 * xs.abs().max()
+    b = torch.randn(n, generator=g).to(BF16)
+    reps = (N + n - 1) // n
+    layer = _layer(wq.repeat(reps, 1)[:N].contiguous(), ws.repeat(reps)[:N].contiguous(), b.repeat(reps)[:N].contiguous())
+    y = _forward(layer, xq, xs).cpu()
+    for first in (0, (N // n - 1) * n):
+        part = y[:, first:first + n].double()
+        ref, size = i8ref.product(xq, xs, wq, ws, b, False)
+        far = ref.abs() > 3.4e38
+        assert far.any() and (~far).any()
+        assert torch.isinf(part[far]).all() and torch.equal(part[far] > 0, ref[far] > 0)
+        near = ref.abs() < 3.3e38  # between the two, rounding decides
+        i8ref.check_y(part[near], ref[near], i8ref.PRODUCT_TOL * size[near], form)
+        assert torch.equal(part[0], b.double())
