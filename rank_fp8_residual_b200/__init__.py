@@ -10,6 +10,9 @@ library has not been built (``python rank_fp8_residual_b200/build.py``).
 from __future__ import annotations
 
 import ctypes
+import itertools
+import math
+import operator
 import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librank_fp8_residual_b200.so")
@@ -292,16 +295,33 @@ def _load_dtypes():
     _BF16, _INT8, _F32 = torch.bfloat16, torch.int8, torch.float32
 
 
-def _buffer(t, what, dtype, n):
-    """Address of an argument of the int8 operators.  A tensor has to be
-    contiguous CUDA memory of that type with n elements (the library sees only
-    its address, so leading dimensions may be split as the caller likes); an
-    integer address is taken as it is."""
+def _regroups(got, rows, cols):
+    """Whether a contiguous tensor of shape `got` can stand for a matrix of rows
+    x cols values.  The library sees only its address, so dimensions may be split
+    and merged as the caller likes (batch x sequence x heads x width, a flat
+    buffer, groups of a row's values as rows of their own); but where the
+    dimensions divide after `cols` elements and not after `rows`, the features
+    come first: a transposed matrix."""
+    if math.prod(got) != rows * cols:
+        return False
+    if rows * cols == 0 or len(got) < 2:
+        return True
+    heads = set(itertools.accumulate(got, operator.mul, initial=1))
+    return rows in heads or cols not in heads
+
+
+def _buffer(t, what, dtype, n, matrix=None):
+    """Address of an argument of the int8 operators, n values; `matrix` is (rows,
+    columns) where it has more than one row.  A tensor has to be contiguous CUDA
+    memory of that type and of a shape that can stand for them; an integer address
+    is taken as it is."""
     if t is None or type(t) is int:
         return t
-    if t.dtype is dtype and t.numel() == n and t.is_cuda and t.is_contiguous():
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (
+            t.numel() == n if matrix is None else t.shape == matrix or _regroups(t.shape, *matrix)):
         return t.data_ptr()
-    raise LLError(LL_ERR_INVALID_ARG, f"{what}: a contiguous CUDA tensor of {dtype} with {n} elements is needed, "
+    raise LLError(LL_ERR_INVALID_ARG, f"{what}: a contiguous CUDA tensor of {dtype} with {n} elements"
+                                      f"{f' in {matrix[0]} rows' if matrix else ''} is needed, "
                                       f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
@@ -315,10 +335,11 @@ def ll_rmsnorm_i8(x, residual, weight, eps: float, M: int, K: int, h, y, codes, 
     if _BF16 is None:
         _load_dtypes()
     M, K, b = int(M), int(K), _BF16
-    n = M * K
-    rc = _lib.ll_rmsnorm_i8(_buffer(x, "x", b, n), _buffer(residual, "residual", b, n),
-                            _buffer(weight, "weight", b, K), eps, M, K, _buffer(h, "h", b, n), _buffer(y, "y", b, n),
-                            _buffer(codes, "codes", _INT8, n), _buffer(scale, "scale", _F32, M), _stream(stream))
+    n, mk = M * K, None if M == 1 else (M, K)
+    rc = _lib.ll_rmsnorm_i8(_buffer(x, "x", b, n, mk), _buffer(residual, "residual", b, n, mk),
+                            _buffer(weight, "weight", b, K), eps, M, K, _buffer(h, "h", b, n, mk),
+                            _buffer(y, "y", b, n, mk), _buffer(codes, "codes", _INT8, n, mk),
+                            _buffer(scale, "scale", _F32, M), _stream(stream))
     if rc != LL_OK:
         raise LLError(rc, "ll_rmsnorm_i8")
 
@@ -329,8 +350,8 @@ def ll_quantize_i8(x, M: int, K: int, codes, scale, stream=None) -> None:
     if _BF16 is None:
         _load_dtypes()
     M, K = int(M), int(K)
-    n = M * K
-    rc = _lib.ll_quantize_i8(_buffer(x, "x", _BF16, n), M, K, _buffer(codes, "codes", _INT8, n),
+    n, mk = M * K, None if M == 1 else (M, K)
+    rc = _lib.ll_quantize_i8(_buffer(x, "x", _BF16, n, mk), M, K, _buffer(codes, "codes", _INT8, n, mk),
                              _buffer(scale, "scale", _F32, M), _stream(stream))
     if rc != LL_OK:
         raise LLError(rc, "ll_quantize_i8")
@@ -401,7 +422,7 @@ class Int8LinearLayer:
     def set_weights(self, codes, scale, bias=None):
         """codes int8 [N, K], scale float32 [N], bias bf16 [N] or None (CUDA)."""
         _load_dtypes()
-        ll_i8_set_weights(self.handle, _buffer(codes, "codes", _INT8, self.N * self.K),
+        ll_i8_set_weights(self.handle, _buffer(codes, "codes", _INT8, self.N * self.K, (self.N, self.K)),
                           _buffer(scale, "scale", _F32, self.N), _buffer(bias, "bias", _BF16, self.N))
 
     @classmethod
@@ -424,8 +445,10 @@ class Int8LinearLayer:
         if out is None:
             import torch
             out = torch.empty(*scale.shape, self.N, dtype=_BF16, device=codes.device)
-        rc = _lib.ll_i8_forward(self.handle, _buffer(codes, "codes", _INT8, M * self.K), _buffer(scale, "scale", _F32, M),
-                                _buffer(out, "out", _BF16, M * self.N), M, _stream(stream))
+        one = M == 1
+        rc = _lib.ll_i8_forward(self.handle, _buffer(codes, "codes", _INT8, M * self.K, None if one else (M, self.K)),
+                                _buffer(scale, "scale", _F32, M),
+                                _buffer(out, "out", _BF16, M * self.N, None if one else (M, self.N)), M, _stream(stream))
         if rc != LL_OK:
             raise LLError(rc, "ll_i8_forward")
         return out
