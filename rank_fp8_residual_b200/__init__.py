@@ -409,8 +409,8 @@ def ll_i8_destroy(h: int) -> None:
 class Int8LinearLayer:
     """Owns one int8 layer: y = bf16(act(scale[m] * w_scale[n] * (codes
     w_codes^T) + bias)).  ``forward(codes, scale)`` takes the int8 codes [..., K]
-    and float32 scale [...] of ll_rmsnorm_i8 or ll_quantize_i8 and returns a new
-    bf16 tensor [..., N] (or ``out``)."""
+    and float32 scale [...] (or [..., 1]) of ll_rmsnorm_i8 or ll_quantize_i8 and
+    returns a new bf16 tensor [..., N] (or ``out``)."""
 
     def __init__(self, N: int, K: int, epilogue: int = LL_EPILOGUE_NONE):
         self.handle = None
@@ -444,7 +444,10 @@ class Int8LinearLayer:
         M = scale.numel()
         if out is None:
             import torch
-            out = torch.empty(*scale.shape, self.N, dtype=_BF16, device=codes.device)
+            rows = scale.shape
+            if codes.dim() > 1 and rows == codes.shape[:-1] + (1,):  # a maximum that kept its dimension
+                rows = rows[:-1]
+            out = torch.empty(*rows, self.N, dtype=_BF16, device=codes.device)
         one = M == 1
         rc = _lib.ll_i8_forward(self.handle, _buffer(codes, "codes", _INT8, M * self.K, None if one else (M, self.K)),
                                 _buffer(scale, "scale", _F32, M),

@@ -55,3 +55,24 @@ def test_vectors_are_counted():
         assert ll._buffer(_Tensor(*shape), "scale", torch.bfloat16, 8) == 4096
     with pytest.raises(ll.LLError):
         ll._buffer(_Tensor(9), "scale", torch.bfloat16, 8)
+
+
+@pytest.mark.parametrize("codes,scale,out", [
+    ((8, 64), (8,), (8, 24)), ((8, 64), (8, 1), (8, 24)), ((2, 4, 64), (2, 4), (2, 4, 24)),
+    ((2, 4, 64), (2, 4, 1), (2, 4, 24)), ((8, 1, 64), (8, 1), (8, 1, 24)), ((64,), (), (24,)), ((64,), (1,), (1, 24)),
+    ((512,), (2, 4), (2, 4, 24)), ((8, 4, 16), (8,), (8, 24)), ((1, 64), (1, 1), (1, 24)), ((0, 64), (0, 1), (0, 24))])
+def test_shape_of_a_forward(monkeypatch, codes, scale, out):
+    """The leading dimensions of the scales, without one that a maximum kept."""
+    calls = []
+
+    class Lib:
+        ll_i8_forward = staticmethod(lambda *a: calls.append(a) or 0)
+        ll_i8_destroy = staticmethod(lambda h: None)
+
+    monkeypatch.setattr(ll, "_lib", Lib)
+    monkeypatch.setattr(ll, "_buffer", lambda t, *a: t)
+    layer = object.__new__(ll.Int8LinearLayer)
+    layer.handle, layer.N, layer.K = 1, 24, 64
+    y = layer.forward(torch.empty(codes, dtype=torch.int8), torch.empty(scale), stream=0)
+    assert y.shape == torch.Size(out) and y.dtype == torch.bfloat16
+    assert calls[0][3] is y and calls[0][4] == y.numel() // 24
