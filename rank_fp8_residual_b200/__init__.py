@@ -118,19 +118,30 @@ def _addr(t):
     return t.data_ptr()
 
 
-_raw_stream = _raw_device = None
+_current_stream = None
+
+
+def _find_current_stream():
+    """A function that gives the handle of torch's current stream: without the
+    Stream object (0.2 against 3.2 us, which a one-token call would feel) where
+    torch has the functions for that, which are not public, else with it."""
+    import torch
+    device = torch.cuda.current_device()  # initialises CUDA
+    try:
+        raw, current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        if raw(current()) == torch.cuda.current_stream(device).cuda_stream:
+            return lambda: raw(current())
+    except (AttributeError, TypeError):
+        pass
+    return lambda: torch.cuda.current_stream().cuda_stream
 
 
 def _stream(s):
     if s is None:
-        # What torch.cuda.current_stream().cuda_stream gives, without the
-        # Stream object (0.2 against 3.2 us, which a one-token call would feel).
-        global _raw_stream, _raw_device
-        if _raw_stream is None:
-            import torch
-            torch.cuda.current_device()  # initialises CUDA
-            _raw_stream, _raw_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-        return _raw_stream(_raw_device())
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
