@@ -147,6 +147,23 @@ def _stream(s):
     return s.cuda_stream
 
 
+def _new_output(shape, dtype, device, stream):
+    """Memory for what a kernel on `stream` (None: the current one) writes, and
+    the current stream may read.  torch hands memory on in the order of the stream
+    that it was taken on: taken on the current one, it could be a tensor's that
+    work still queued there uses."""
+    import torch
+    if stream is not None:
+        current, handle = torch.cuda.current_stream(device), _stream(stream)
+        if handle != current.cuda_stream:
+            with torch.cuda.stream(torch.cuda.ExternalStream(handle, device) if handle
+                                   else torch.cuda.default_stream(device)):
+                out = torch.empty(shape, dtype=dtype, device=device)
+            out.record_stream(current)
+            return out
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
 def status_string(code: int) -> str:
     return _lib.ll_status_string(int(code)).decode()
 
@@ -454,11 +471,10 @@ class Int8LinearLayer:
             _load_dtypes()
         M = scale.numel()
         if out is None:
-            import torch
             rows = scale.shape
             if codes.dim() > 1 and rows == codes.shape[:-1] + (1,):  # a maximum that kept its dimension
                 rows = rows[:-1]
-            out = torch.empty(*rows, self.N, dtype=_BF16, device=codes.device)
+            out = _new_output((*rows, self.N), _BF16, codes.device, stream)
         one = M == 1
         rc = _lib.ll_i8_forward(self.handle, _buffer(codes, "codes", _INT8, M * self.K, None if one else (M, self.K)),
                                 _buffer(scale, "scale", _F32, M),
@@ -515,7 +531,7 @@ class LiteLinearLayer:
         import torch
         M = x.shape[0]
         if out is None:
-            out = torch.empty(M, self.out_features, dtype=torch.bfloat16, device=x.device)
+            out = _new_output((M, self.out_features), torch.bfloat16, x.device, stream)
         ll_forward(self.handle, x, out, M, stream)
         return out
 

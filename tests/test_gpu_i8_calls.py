@@ -35,3 +35,73 @@ def test_transposed_matrices_are_refused():
     assert torch.equal(layer.forward(xq.view(M, 4, 16), xs), want)
     ll.ll_quantize_i8(x, 4 * M, K // 4, c, torch.empty(4 * M, device="cuda"))
     assert torch.equal(c.cpu().view(4 * M, K // 4), i8ref.codes_of(x.cpu().view(4 * M, K // 4))[0])
+
+
+def _layers():
+    from synth_inputs import make_inputs
+    ins = _product_inputs(40, 512, 264, 5)
+    inp = make_inputs(40, 512, 264, 16, seed=6)
+    lite = ll.LiteLinearLayer(264, 512, 16, inp.scale_mode)
+    lite.set_weights(inp.A.cuda(), inp.B.cuda(), inp.Q.cuda(), inp.scale.cuda(), inp.bias.cuda())
+    return [(_layer(*ins[2:]), (ins[0].cuda(), ins[1].cuda())), (lite, (inp.x.cuda(),))]
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_a_new_output_of_another_stream(which, as_handle):
+    """An output made for a forward on another stream is not memory that the
+    current stream still writes, nor does a later one take it over while the
+    current stream still reads it."""
+    layer, args = _layers()[which]
+    want = layer.forward(*args)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if as_handle else side
+    torch.cuda.synchronize()
+    before = torch.empty_like(want)
+    torch.cuda._sleep(100_000_000)  # keeps the current stream busy for some 50 ms
+    before.fill_(7.0)
+    taken = before.data_ptr()
+    del before
+    out = layer.forward(*args, stream=stream)
+    assert out.data_ptr() != taken
+    side.synchronize()
+    assert torch.equal(out.cpu(), want.cpu())
+    torch.cuda._sleep(100_000_000)
+    copy, taken = out.clone(), out.data_ptr()
+    del out
+    again = layer.forward(*args, stream=stream)
+    assert again.data_ptr() != taken
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want) and torch.equal(again, want)
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_a_new_output_of_a_captured_forward(which):
+    layer, args = _layers()[which]
+    want = layer.forward(*args)
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        out = layer.forward(*args, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        copy = out.clone()
+    for _ in range(2):
+        out.zero_()
+        copy.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(copy, want)
+
+
+def test_streams_given_as_zero_and_as_the_current_one():
+    layer, args = _layers()[0]
+    want = layer.forward(*args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = [layer.forward(*args, stream=side), layer.forward(*args)]
+        torch.cuda.synchronize()
+        got.append(layer.forward(*args, stream=0))
+        torch.cuda.synchronize()
+    assert all(torch.equal(t, want) for t in got)

@@ -71,8 +71,12 @@ def test_shape_of_a_forward(monkeypatch, codes, scale, out):
 
     monkeypatch.setattr(ll, "_lib", Lib)
     monkeypatch.setattr(ll, "_buffer", lambda t, *a: t)
+    monkeypatch.setattr(ll, "_stream", lambda s: 0)
     layer = object.__new__(ll.Int8LinearLayer)
     layer.handle, layer.N, layer.K = 1, 24, 64
-    y = layer.forward(torch.empty(codes, dtype=torch.int8), torch.empty(scale), stream=0)
+    try:
+        y = layer.forward(torch.empty(codes, dtype=torch.int8), torch.empty(scale))
+    finally:
+        layer.handle = None  # never the library's
     assert y.shape == torch.Size(out) and y.dtype == torch.bfloat16
     assert calls[0][3] is y and calls[0][4] == y.numel() // 24
