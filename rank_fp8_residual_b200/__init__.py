@@ -156,8 +156,8 @@ def _new_output(shape, dtype, device, stream):
     if stream is not None:
         current, handle = torch.cuda.current_stream(device), _stream(stream)
         if handle != current.cuda_stream:
-            with torch.cuda.stream(torch.cuda.ExternalStream(handle, device) if handle
-                                   else torch.cuda.default_stream(device)):
+            with torch.cuda.stream(torch.cuda.ExternalStream(handle, device) if handle > 1
+                                   else torch.cuda.default_stream(device)):  # 0, or cudaStreamLegacy
                 out = torch.empty(shape, dtype=dtype, device=device)
             out.record_stream(current)
             return out

@@ -94,6 +94,19 @@ def test_a_new_output_of_a_captured_forward(which):
         assert torch.equal(out, want) and torch.equal(copy, want)
 
 
+@pytest.mark.parametrize("handle", [0, 1, 2])
+def test_new_outputs_of_the_streams_that_have_a_number(handle):
+    """The default stream, as 0 and as cudaStreamLegacy, and cudaStreamPerThread."""
+    layer, args = _layers()[0]
+    want = layer.forward(*args)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = layer.forward(*args, stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
 def test_streams_given_as_zero_and_as_the_current_one():
     layer, args = _layers()[0]
     want = layer.forward(*args)
