@@ -385,15 +385,38 @@ def ll_quantize_i8(x, M: int, K: int, codes, scale, stream=None) -> None:
         raise LLError(rc, "ll_quantize_i8")
 
 
+_i8_sizes = {}  # (N, K) of each int8 layer that lives
+
+
+def _i8_size(h, what):
+    """(N, K) of a layer; nothing else is one (a destroyed one's memory is gone)."""
+    if h not in _i8_sizes:
+        raise LLError(LL_ERR_INVALID_ARG, f"{what}: {h} is no int8 layer")
+    return _i8_sizes[h]
+
+
+def _room(t, what, dtype, n):
+    """As _buffer, of a tensor whose first n values are meant."""
+    if t is None or type(t) is int or t.dtype is dtype and t.numel() >= n and t.is_cuda and t.is_contiguous():
+        return _addr(t)
+    raise LLError(LL_ERR_INVALID_ARG, f"{what}: a contiguous CUDA tensor of {dtype} with {n} elements or more is needed, "
+                                      f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
 def ll_i8_create(N: int, K: int) -> int:
     h = _lib.ll_i8_create(int(N), int(K))
     if not h:
         raise LLError(_lib.ll_last_error(), "ll_i8_create")
+    _i8_sizes[h] = int(N), int(K)
     return h
 
 
 def ll_i8_set_weights(h: int, codes, scale, bias=None) -> None:
-    rc = _lib.ll_i8_set_weights(h, _addr(codes), _addr(scale), _addr(bias))
+    """codes int8 [N, K], scale float32 [N], bias bf16 [N] or None."""
+    N, K = _i8_size(h, "ll_i8_set_weights")
+    _load_dtypes()
+    rc = _lib.ll_i8_set_weights(h, _room(codes, "codes", _INT8, N * K), _room(scale, "scale", _F32, N),
+                                _room(bias, "bias", _BF16, N))
     if rc != LL_OK:
         raise LLError(rc, "ll_i8_set_weights")
 
@@ -405,7 +428,13 @@ def ll_i8_set_epilogue(h: int, epilogue: int) -> None:
 
 
 def ll_i8_forward(h: int, codes, scale, y, M: int, stream=None) -> None:
-    rc = _lib.ll_i8_forward(h, _addr(codes), _addr(scale), _addr(y), int(M), _stream(stream))
+    """y bf16 [M, N] of codes int8 [M, K] and scale float32 [M]: the first M
+    rows of what is given."""
+    N, K = _i8_size(h, "ll_i8_forward")
+    _load_dtypes()
+    M = int(M)
+    rc = _lib.ll_i8_forward(h, _room(codes, "codes", _INT8, M * K), _room(scale, "scale", _F32, M),
+                            _room(y, "y", _BF16, M * N), M, _stream(stream))
     if rc != LL_OK:
         raise LLError(rc, "ll_i8_forward")
 
@@ -431,6 +460,7 @@ def ll_i8_set_debug(h: int, withhold_producer: bool, timeout_ns: int) -> None:
 
 
 def ll_i8_destroy(h: int) -> None:
+    _i8_sizes.pop(h, None)
     _lib.ll_i8_destroy(h)
 
 
