@@ -187,6 +187,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   const int pid = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
   const int tiles = p.na * p.nb;
   const int w = p.w, slot_bytes = i8_slot_bytes(w), stages = i8_stages(w);
+  bool done = true;  // no wait of this thread ran out
 
   if (warp == 0) {
     // ------------------------------------------- TMA producer (both CTAs)
@@ -227,14 +228,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
         if (++slot == stages) { slot = 0; ph ^= 1; }
       }
     }
-    if (!ok && !p.withhold) {
-      // Loads already issued must land before the CTA exits; they
-      // complete on leader barriers whose other arrivals may never come
-      // now, so wait a bounded settle time far above any load latency.
-      const uint64_t c0 = clock_cycles();
-      while (clock_cycles() - c0 < 400000ull) {  // >= 200 us at any clock up to 2 GHz
-      }
-    }
+    done = ok;
   } else if (warp == 1) {
     if (leader) {
       // --------------------------------------------- MMA issuer (leader)
@@ -266,6 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       commit_one_pair(drain, 0x1, one);
       if (one) mbar_wait_drain(drain, 0, p.watch);
       __syncwarp();
+      done = ok;
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -304,7 +299,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
         i8_token_scales(sx, p.sx, b0 + 16 * half, p.M);
       else if (32 * half < w)
         load_sb(32 * half);
-      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], (it >> 1) & 1, p.watch, kErrTimeoutEpilogue))) break;
+      done = __all_sync(0xffffffffu, mbar_wait(&tfull[buf], (it >> 1) & 1, p.watch, kErrTimeoutEpilogue));
+      if (!done) break;
       tc_fence_after();
       const uint32_t acc = tl + 256u * buf;
       if constexpr (kSwap) {
@@ -357,7 +353,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   }
 
   tc_fence_before();
-  __syncthreads();
+  // Where a wait ran out, loads that the producer has issued may be in flight,
+  // and the barriers of the leader that they complete on never be waited for:
+  // they must land before the CTA exits.
+  if (!__syncthreads_and(done) && !p.withhold) settle();
   cluster_sync();  // the pair's MMAs and epilogues are done with both TMEMs
   if (warp == 1) {
     tc_fence_after();
@@ -407,7 +406,8 @@ __host__ __device__ constexpr int is_smem_bytes(int Mt, int ring) {
 // go through shared memory ([token][feature]), and the CTAs of the cluster add
 // them over distributed shared memory, each for every splits-th token.
 template <int kAct, int kEpiWarps>
-__global__ void __launch_bounds__(is_threads(kEpiWarps), 1) ll_i8_stream_kernel(const __grid_constant__ I8StreamParams p) {
+__global__ void __launch_bounds__(is_threads(kEpiWarps), kEpiWarps > 8 ? 2 : 1)
+    ll_i8_stream_kernel(const __grid_constant__ I8StreamParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = align1024(smem_raw);
   const int sb = is_stage_bytes(p.Mt), ns = p.stages;
@@ -469,8 +469,6 @@ __global__ void __launch_bounds__(is_threads(kEpiWarps), 1) ll_i8_stream_kernel(
         load_2d_one(ring0 + slot * sb + 16384, &p.tm_x, full0 + 8u * slot, (s0 + i) * 128, 0, one);
         if (++slot == ns) { slot = 0; ph ^= 1; }
       }
-      if (!ok)  // let every load already issued land before the CTA can exit
-        for (int j = max(0, i - ns); j < i; ++j) mbar_wait_drain(&full[j % ns], (j / ns) & 1, p.watch);
     }
   } else if (warp == 1) {
     const uint32_t one = elect_one();
@@ -479,7 +477,8 @@ __global__ void __launch_bounds__(is_threads(kEpiWarps), 1) ll_i8_stream_kernel(
     int slot = 0;
     uint32_t ph = 0;
     for (int i = 0; i < n; ++i) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], ph, p.watch, kErrTimeoutMma))) break;
+      ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], ph, p.watch, kErrTimeoutMma));
+      if (!ok) break;
       tc_fence_after();
       const uint64_t dw = dw0 + static_cast<uint64_t>(slot * (sb >> 4)), dx = dx0 + static_cast<uint64_t>(slot * (sb >> 4));
 #pragma unroll
@@ -531,6 +530,7 @@ __global__ void __launch_bounds__(is_threads(kEpiWarps), 1) ll_i8_stream_kernel(
   }
   tc_fence_before();
   ok = __syncthreads_and(ok);
+  if (!ok && !p.withhold) settle();  // loads that are in flight must land before the CTA exits
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tbase, p.tmem_cols);

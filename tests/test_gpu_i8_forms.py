@@ -82,3 +82,23 @@ def test_scales_far_from_one_on_every_form(nk, form, M):
         near = ref.abs() < 3.3e38  # between the two, rounding decides
         i8ref.check_y(part[near], ref[near], i8ref.PRODUCT_TOL * size[near], form)
         assert torch.equal(part[0], b.double())
+
+
+@pytest.mark.parametrize("nk,form,M", CASES)
+def test_waits_that_run_out_while_the_loads_arrive(nk, form, M):
+    """With a limit of a nanosecond any wait may give up while the kernel's own
+    loads and products are on their way: it lets them end, tells so, and the layer
+    works on.  (What such a forward gives is not looked at.)"""
+    N, K = nk
+    xq, xs, wq, ws, b = _product_inputs(M, K, N, 9)
+    layer = _layer(wq, ws, b)
+    want = _forward(layer, xq, xs)
+    x, s = xq.cuda(), xs.cuda()
+    for _ in range(3):
+        ll.ll_i8_set_debug(layer.handle, False, 1)
+        for _ in range(4):
+            layer.forward(x, s)
+        torch.cuda.synchronize()
+        assert ll.ll_i8_status(layer.handle) in (ll.LL_OK, ll.LL_ERR_DEVICE_TIMEOUT)
+        ll.ll_i8_set_debug(layer.handle, False, 2_000_000_000)
+        assert torch.equal(_forward(layer, xq, xs), want)
