@@ -105,7 +105,6 @@ struct I8Params {
   CUtensorMap tm_y;  // bf16 y [M, N] box {32, 32}, 64B swizzle, or {32, 16} without (kSwap)
   const float* sx;       // [M]
   const float4* sb;      // [N rounded up / 2] (scale, scale, bias, bias) of two features
-  uint16_t* y;           // [M, N] bf16 bits
   int M, N, K;
   int na, nb;            // tiles of a and b
   int w;                 // rows of b per tile: a multiple of 32, 64..256

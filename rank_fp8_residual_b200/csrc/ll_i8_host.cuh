@@ -174,8 +174,11 @@ constexpr int kI8StreamMaxM = 256;  // the MMA's N
 //   kernel: 310, 367 and 565 cycles per K step), the weight at 5.7 TB/s;
 //   products of a 256 x w step take 2.2 w cycles (2 w alone);
 //   start and end cost 5,000 (pair) or 5,560 (streaming), and the last tile's
-//   epilogue 4,500 per 256 columns (11,000 with kSwap's stores token by token)
-//   or 42 per token (streaming), 5 % of which starts under the kernel before;
+//   epilogue 4,500 per 256 columns (10,000 with kSwap: its shuffles and scales
+//   token by token, and what a choice against measured crossovers leaves open: over
+//   some 150 sizes of up to 3630 tokens every plan that 11,000 chose otherwise
+//   was slower, 100 x 1024 -> 28000 12.3 against 9.8 us) or 42 per token
+//   (streaming), 5 % of which starts under the kernel before;
 //   a streaming launch with 16 epilogue warps all but hides them (60 per token
 //   above 25).
 struct I8Plan {
@@ -199,7 +202,7 @@ I8Plan i8_plan_pair(const ll_i8_layer* h, int M) {
       const int nb = (b + w - 1) / w;
       const double waves = std::ceil(static_cast<double>(na) * nb / pairs);
       const double loop = waves * (steps * std::max(2.2 * w, (16384.0 + 64.0 * w) / 66.0) + 200.0);
-      const double cycles = 5000.0 + std::max(loop, i8_weight_cycles(h)) + (swap ? 11000.0 : 4500.0) * w / 256;
+      const double cycles = 5000.0 + std::max(loop, i8_weight_cycles(h)) + (swap ? 10000.0 : 4500.0) * w / 256;
       if (best.cycles < 0 || cycles < 0.98 * best.cycles) best = I8Plan{false, 0, 0, swap, na, nb, w, cycles};
     }
   }
@@ -312,7 +315,6 @@ int launch_i8(const ll_i8_layer* h, const I8Plan& plan, const void* codes, const
   p.tm_w = weight_map(h, plan.swap ? 128 : p.w / 2);
   p.sx = scale;
   p.sb = h->sb;
-  p.y = static_cast<uint16_t*>(y);
   p.M = M;
   p.N = h->N;
   p.K = h->K;

@@ -11,3 +11,14 @@ def test_cases_are_planned_on_their_forms(nk, form, M):
 
 def test_every_form_has_a_case():
     assert {form for _, form, _ in forms.CASES} == {forms.SPLIT, forms.DIRECT, forms.STAGED, forms.PAIR, forms.SWAP}
+
+
+@pytest.mark.parametrize("M,K,N,form", [
+    # us, this form and the next best of another
+    (100, 1024, 28000, forms.SWAP),  # 9.8, 11.5 streaming, 12.3 pairs
+    (65, 1024, 28000, forms.SWAP),   # 9.1, 11.0 streaming
+    (65, 2048, 8192, forms.SWAP),    # 7.3, 7.7 streaming
+    (257, 4096, 8192, forms.SWAP),   # 12.7, 14.7 pairs
+    (200, 1040, 18936, forms.PAIR), (640, 1024, 28000, forms.PAIR), (65, 4096, 8192, forms.SPLIT)])
+def test_measured_crossovers_of_the_swapped_pairs(M, K, N, form):
+    assert forms.form_of(N, K, M) == form
