@@ -2,12 +2,14 @@
 streaming (straight stores and staged ones), CTA pairs in both orientations.
 The cases name the form that they are meant for, and test_i8_forms_plan checks
 that they are planned so."""
+import math
+
 import pytest
 import torch
 
 import i8ref
 import rank_fp8_residual_b200 as ll
-from test_gpu_i8 import _forward, _layer, _product_inputs
+from test_gpu_i8 import _block, _check_product, _forward, _layer, _product_inputs
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -18,6 +20,16 @@ NARROW = (2056, 2064)
 WIDE = (16392, 4096)
 FORMS = {NARROW: {SPLIT: 20, PAIR: 300}, WIDE: {DIRECT: 5, STAGED: 40, SWAP: 300, PAIR: 512}}
 CASES = [(nk, form, M) for nk, forms in FORMS.items() for form, M in forms.items()]
+
+
+# Shapes (M, K, N) with a part of a tile left over in every direction
+REMAINDERS = {SPLIT: [(20, 2064, 2056), (100, 8208, 2056)], DIRECT: [(31, 1040, 18936), (5, 4112, 16392)],
+              STAGED: [(40, 4112, 16392), (77, 1040, 18936), (130, 144, 18936)],
+              PAIR: [(300, 2064, 2056), (513, 1040, 18936), (1025, 528, 3000)],
+              SWAP: [(300, 4112, 16392), (80, 2064, 8200), (257, 1040, 18936)]}
+# Feed-forwards (M, K, F) whose first product is of a form
+STEPS = {SPLIT: (20, 512, 1536), DIRECT: (3, 512, 18944), STAGED: (40, 512, 18944), PAIR: (200, 512, 18944),
+         SWAP: (257, 1040, 18944)}
 
 
 def form_of(N, K, M, num_sms=148):
@@ -102,3 +114,106 @@ def test_waits_that_run_out_while_the_loads_arrive(nk, form, M):
         assert ll.ll_i8_status(layer.handle) in (ll.LL_OK, ll.LL_ERR_DEVICE_TIMEOUT)
         ll.ll_i8_set_debug(layer.handle, False, 2_000_000_000)
         assert torch.equal(_forward(layer, xq, xs), want)
+
+
+@pytest.mark.parametrize("gelu", [False, True])
+@pytest.mark.parametrize("form,shape", [(f, s) for f, shapes in REMAINDERS.items() for s in shapes])
+def test_product_with_remainders(form, shape, gelu):
+    _check_product(*shape, bias=not gelu or form != PAIR, gelu=gelu, seed=sum(shape))
+
+
+@pytest.mark.parametrize("nk,form,M", CASES)
+def test_withheld_loads_time_out_on_every_form(nk, form, M):
+    N, K = nk
+    xq, xs, wq, ws, b = _product_inputs(M, K, N, 10)
+    layer = _layer(wq, ws, b)
+    want = _forward(layer, xq, xs)
+    x, s = xq.cuda(), xs.cuda()
+    ll.ll_i8_set_debug(layer.handle, True, 1_000_000)
+    layer.forward(x, s)
+    torch.cuda.synchronize()
+    assert ll.ll_i8_status(layer.handle) == ll.LL_ERR_DEVICE_TIMEOUT
+    ll.ll_i8_set_debug(layer.handle, False, 2_000_000_000)
+    assert torch.equal(_forward(layer, xq, xs), want)
+
+
+@pytest.mark.parametrize("nk,form,M", CASES)
+def test_nan_scales_on_every_form(nk, form, M):
+    N, K = nk
+    xq, xs, wq, ws, b = _product_inputs(M, K, N, 11)
+    layer = _layer(wq, ws, b, gelu=True)
+    want = _forward(layer, xq, xs).cpu()
+    for m in (0, M // 2, M - 1):
+        bad = xs.clone()
+        bad[m] = math.nan
+        y = _forward(layer, xq, bad).cpu()
+        assert torch.isnan(y[m]).all()
+        keep = torch.arange(M) != m
+        assert torch.equal(y[keep], want[keep])
+
+
+@pytest.mark.parametrize("form", list(STEPS))
+def test_steps_one_by_one_back_to_back_and_replayed(form):
+    """Steps of a feed-forward whose first product is of the form, each kernel
+    allowed to start under the end of the one before: the same bits as with a
+    wait after every call."""
+    M, K, F = STEPS[form]
+    results = []
+    for mode in range(3):
+        t, step = _block(M, K, F, 81)
+        torch.cuda.synchronize()
+        if mode == 0:
+            for _ in range(12):
+                step(torch.cuda.synchronize)
+        elif mode == 1:
+            for _ in range(12):
+                step()
+        else:
+            h0, d0 = t["h"].clone(), t["d"].clone()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                for _ in range(6):
+                    step()
+            t["h"].copy_(h0)
+            t["d"].copy_(d0)
+            g.replay()
+            g.replay()
+        torch.cuda.synchronize()
+        results.append((t["h"].cpu(), t["d"].cpu()))
+    for r in results[1:]:
+        assert torch.equal(r[0], results[0][0]) and torch.equal(r[1], results[0][1])
+    assert torch.isfinite(results[0][0].float()).all()
+
+
+@pytest.mark.parametrize("nk,form,M", CASES)
+def test_one_layer_on_two_streams_and_in_two_graphs(nk, form, M):
+    """Forwards of a layer on two streams at once, each with its own tokens."""
+    N, K = nk
+    xq, xs, wq, ws, b = _product_inputs(2 * M, K, N, 12)
+    layer = _layer(wq, ws, b)
+    want = [_forward(layer, xq[k * M:(k + 1) * M], xs[k * M:(k + 1) * M]) for k in range(2)]
+    dev = [(xq[k * M:(k + 1) * M].cuda(), xs[k * M:(k + 1) * M].cuda()) for k in range(2)]
+    outs = [torch.zeros(M, N, dtype=BF16, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(15):
+        for k in range(2):
+            layer.forward(*dev[k], out=outs[k], stream=streams[k])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    graphs = []
+    for k in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=streams[k]):
+            for _ in range(3):
+                layer.forward(*dev[k], out=outs[k])
+        graphs.append(g)
+        outs[k].zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for k, g in enumerate(graphs):
+            with torch.cuda.stream(streams[k]):
+                g.replay()
+    torch.cuda.synchronize()
+    assert ll.ll_i8_status(layer.handle) == ll.LL_OK
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
