@@ -28,6 +28,19 @@ namespace llk {
 
 constexpr int kI8MaxK = 131056;
 
+// A time far above any load's or MMA's latency, that a CTA's own ones in flight
+// get to complete after an error, whatever the limit of the waits.
+constexpr uint64_t kI8SettleCycles = 400000;  // >= 200 us at any clock up to 2 GHz
+__device__ __forceinline__ void i8_settle() {
+  const uint64_t c0 = clock_cycles();
+  while (clock_cycles() - c0 < kI8SettleCycles) {
+  }
+}
+// The wait for the MMAs in flight (the barrier's only arrival is their commit's).
+__device__ __forceinline__ void i8_drain(uint64_t* bar, const Watch& w) {
+  mbar_wait_drain(bar, 0, Watch{w.status, max(w.timeout_ns, kI8SettleCycles / 2)});
+}
+
 // Two outputs from their sums: scaled by their tokens' scales sm, then s =
 // (scale, scale, bias, bias) of their features.  The sum takes one scale after
 // the other, as the formula's factors may be far from 1 where their product with
@@ -257,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       }
       // No MMA may still run when TMEM is released.
       commit_one_pair(drain, 0x1, one);
-      if (one) mbar_wait_drain(drain, 0, p.watch);
+      if (one) i8_drain(drain, p.watch);
       __syncwarp();
       done = ok;
     }
@@ -355,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   // Where a wait ran out, loads that the producer has issued may be in flight,
   // and the barriers of the leader that they complete on never be waited for:
   // they must land before the CTA exits.
-  if (!__syncthreads_and(done) && !p.withhold) settle();
+  if (!__syncthreads_and(done) && !p.withhold) i8_settle();
   cluster_sync();  // the pair's MMAs and epilogues are done with both TMEMs
   if (warp == 1) {
     tc_fence_after();
@@ -487,7 +500,7 @@ __global__ void __launch_bounds__(is_threads(kEpiWarps), kEpiWarps > 8 ? 2 : 1)
       if (++slot == ns) { slot = 0; ph ^= 1; }
     }
     commit_one(drain, one);
-    if (one) mbar_wait_drain(drain, 0, p.watch);
+    if (one) i8_drain(drain, p.watch);
     __syncwarp();
   } else {
     // TMEM lane = feature, column = token; the warps of a lane quadrant take
@@ -529,7 +542,7 @@ __global__ void __launch_bounds__(is_threads(kEpiWarps), kEpiWarps > 8 ? 2 : 1)
   }
   tc_fence_before();
   ok = __syncthreads_and(ok);
-  if (!ok && !p.withhold) settle();  // loads that are in flight must land before the CTA exits
+  if (!ok && !p.withhold) i8_settle();  // loads that are in flight must land before the CTA exits
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tbase, p.tmem_cols);

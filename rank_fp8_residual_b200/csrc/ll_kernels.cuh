@@ -50,23 +50,13 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-// A time far above any load's or MMA's latency, that a CTA's own ones in flight
-// get to complete after an error, whatever the limit of the waits.
-constexpr uint64_t kSettleCycles = 400000;  // >= 200 us at any clock up to 2 GHz
-__device__ __forceinline__ void settle() {
-  const uint64_t c0 = clock_cycles();
-  while (clock_cycles() - c0 < kSettleCycles) {
-  }
-}
-
 // Bounded wait used while draining after an error: ignores the status
-// word, gives up after the timeout, but not before own work in flight can
-// have ended.
+// word, gives up after the timeout.
 __device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity, const Watch& w) {
   const uint32_t a = smem_u32(bar);
   const uint64_t t0 = clock_cycles();
   while (!mbar_try_wait(a, parity)) {
-    if (clock_cycles() - t0 > max(2ull * w.timeout_ns, static_cast<unsigned long long>(kSettleCycles))) {
+    if (clock_cycles() - t0 > 2ull * w.timeout_ns) {
       atomicCAS(w.status, 0, kErrTimeoutDrain);
       return;
     }
