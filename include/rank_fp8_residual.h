@@ -212,7 +212,8 @@ int ll_plan(int N, int K, int r, int M, int num_sms, int variant, int *kernel, i
  * the status clears it. */
 int ll_status(ll_handle h);
 
-/* No counterpart on the pages.  Debug controls: timeout_ns bounds every device-side wait (default 2 s);
+/* No counterpart on the pages.  Debug controls: timeout_ns bounds every device-side wait (default 2 s;
+ * a limit below 200 us is taken as 200 us, the time that copies in flight have after an error);
  * withhold_producer != 0 makes the main kernel's loader issue nothing, so
  * its consumers run into the timeout (used to test the timeout path). */
 int ll_set_debug(ll_handle h, int withhold_producer, uint64_t timeout_ns);
@@ -454,7 +455,8 @@ int ll_i8_forward(ll_i8_handle h, const void *codes, const float *scale, void *y
 enum { LL_I8_STREAM = 0, LL_I8_PAIR = 1, LL_I8_PAIR_SWAP = 2 };
 int ll_i8_plan(int N, int K, int M, int num_sms, int *kernel, int *tile_features, int *tile_tokens, int *splits);
 
-/* As ll_status, ll_set_debug and ll_destroy, for an int8 layer. */
+/* As ll_status, ll_set_debug and ll_destroy, for an int8 layer (any limit is
+ * taken as it is: the 200 us for copies in flight are apart from it). */
 int ll_i8_status(ll_i8_handle h);
 int ll_i8_set_debug(ll_i8_handle h, int withhold_producer, uint64_t timeout_ns);
 void ll_i8_destroy(ll_i8_handle h);

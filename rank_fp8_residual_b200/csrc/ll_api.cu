@@ -1587,7 +1587,9 @@ int ll_set_debug(ll_handle h, int withhold_producer, uint64_t timeout_ns) {
   g_last_error = LL_OK;
   if (!h || timeout_ns == 0) return fail(LL_ERR_INVALID_ARG);
   h->withhold = withhold_producer ? 1 : 0;
-  h->timeout_ns = timeout_ns;
+  // The limit also bounds the waits for copies and MMAs in flight after an
+  // error, which must have ended when a CTA leaves.
+  h->timeout_ns = std::max<uint64_t>(timeout_ns, 200000);
   return LL_OK;
 }
 

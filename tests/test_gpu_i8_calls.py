@@ -118,3 +118,13 @@ def test_streams_given_as_zero_and_as_the_current_one():
         got.append(layer.forward(*args, stream=0))
         torch.cuda.synchronize()
     assert all(torch.equal(t, want) for t in got)
+
+
+def test_a_low_rank_layer_takes_no_limit_below_that_of_copies_in_flight():
+    layer, args = _layers()[1]
+    want = layer.forward(*args)
+    ll.ll_set_debug(layer.handle, False, 1)
+    got = [layer.forward(*args) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert ll.ll_status(layer.handle) == ll.LL_OK
+    assert all(torch.equal(t, want) for t in got)
