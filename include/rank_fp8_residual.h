@@ -401,7 +401,8 @@ int ll_rmsnorm_i8(const void *x, const void *residual, const void *weight, float
 /* Per-row int8 quantisation: a[m] = max_k |x[m, k]|, codes[m, k] = the
  * integer nearest to 127 x[m, k] / a[m] (ties to even), scale[m] = a[m] / 127.
  * x bf16 [M, K], codes int8 [M, K], scale fp32 [M].  For activations (a row
- * is a token) and for a dense weight (a row is an output feature).  Rows of
+ * is a token) and for a dense weight (a row is an output feature; K <= 65536
+ * here, while the layer takes codes of longer ones).  Rows of
  * zeros, NaN and infinities, and errors, as ll_rmsnorm_i8. */
 int ll_quantize_i8(const void *x, int M, int K, void *codes, float *scale, void *stream);
 

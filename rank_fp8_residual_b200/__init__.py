@@ -486,7 +486,8 @@ class Int8LinearLayer:
     @classmethod
     def from_dense(cls, W, bias=None, epilogue: int = LL_EPILOGUE_NONE):
         """A layer from a dense CUDA bf16 weight [out, in], quantised per
-        output feature by ll_quantize_i8."""
+        output feature by ll_quantize_i8, whose rows hold 65536 values at most
+        (LL_ERR_UNSUPPORTED beyond; set_weights takes codes up to 131056)."""
         import torch
         N, K = W.shape
         codes = torch.empty(N, K, dtype=torch.int8, device=W.device)

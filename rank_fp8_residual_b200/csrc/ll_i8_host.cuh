@@ -240,17 +240,19 @@ I8Plan i8_plan_stream(const ll_i8_layer* h, int M) {
     p.cycles = 0.95 * (loop + 5560.0 + 42.0 * M);
   else if (waves == 1)
     p.cycles = loop + 60.0 * M - 1500.0;
-  else  // one CTA per SM: its rounds follow one another (us, streaming / pair: 40 x 4096 -> 19000 20.7 / 18.6, 64 x 1024 ->
-        // 28000 10.2 / 12.9, 64 x 128 -> 19000 3.4 / 6.4)
+  else  // one CTA per SM: its rounds follow one another (us, streaming / pair / swapped: 40 x 4096 -> 19000 22.7 / 22.3 /
+        // 20.4, 64 x 1024 -> 28000 10.2 / 12.5 / 8.7, 64 x 128 -> 19000 3.6 / 6.3 / 4.8)
     p.cycles = 0.95 * std::max(waves * (p.steps * step + std::min(5800.0, 2000.0 + 450.0 * p.steps)),
                                i8_weight_cycles(h));
   return p;
 }
 
-// Measured (us, streaming / pair): 1024 -> 1024: M = 32 4.1 / 4.6, 128 6.0 /
-// 4.7; 4096 -> 4096: 64 7.0 / 9.8, 256 11.4 / 9.6; 4096 -> 16384: 96 14.0 /
-// 16.2, 160 16.3 / 17.6, 200 18.6 / 17.5, 256 19.7 / 17.9; 1024 -> 16384: 128
-// 5.9 / 7.8; 8192 -> 8192: 100 16.4 / 16.2; 8192 -> 2048: 256 12.8 / 14.6.
+// Measured (us, streaming / pair / swapped, the best width of each): 1024 ->
+// 1024: M = 128 6.1 / 4.4 / 4.6; 4096 -> 4096: 64 7.8 / 9.6 / 8.8, 256 12.1 /
+// 9.6 / 10.1; 4096 -> 16384: 96 13.8 / 16.5 / 14.7, 160 15.2 / 16.7 / 16.2, 200
+// 17.9 / 17.3 / 18.1, 256 18.5 / 17.4 / 18.8; 1024 -> 16384: 128 6.8 / 9.0 / 8.4;
+// 2048 -> 8192: 65 7.7 / 8.1 / 7.3; 8192 -> 8192: 100 16.1 / 16.8 / 16.0; 8192 ->
+// 2048: 256 13.6 / 14.1 / 13.8.
 I8Plan i8_plan(const ll_i8_layer* h, int M) {
   const I8Plan pair = i8_plan_pair(h, M);
   if (M > kI8StreamMaxM) return pair;

@@ -181,7 +181,9 @@ __device__ __forceinline__ void norm_row_far(const RowsParams& p, unsigned m) {
 // blocks of up to 256 threads.  Beyond, that would cost the second block on an
 // SM, so h stays, packed, and the products are taken once more (4000 x 16384
 // with residual 68.8 us by 512 threads, 90 with u kept; by 256 68.7, without
-// residual 47.5 and 42.7).
+// residual 47.5 and 42.7).  Rows of more than 16384 values are those of 512 to
+// 1024 threads, one block on an SM: 4000 x 24576 158 us with residual (the bytes
+// take 107), 108 without (46); 2000 x 65536 182 (142) and 116 (61).
 //
 // One or two chunks serve batches of few rows, where registers are free and
 // loads in flight are not: the second bound lets the compiler use 64 (1000 x

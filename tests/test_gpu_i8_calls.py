@@ -128,3 +128,12 @@ def test_a_low_rank_layer_takes_no_limit_below_that_of_copies_in_flight():
     torch.cuda.synchronize()
     assert ll.ll_status(layer.handle) == ll.LL_OK
     assert all(torch.equal(t, want) for t in got)
+
+
+def test_dense_weights_beyond_the_quantisations_rows_are_refused():
+    W = torch.zeros(8, 65552, dtype=BF16, device="cuda")
+    assert _code(lambda: ll.Int8LinearLayer.from_dense(W)) == ll.LL_ERR_UNSUPPORTED
+    W = W[:, :65536].contiguous()
+    W[:, 0] = 1.0
+    c, s = torch.ones(1, 65536, dtype=torch.int8, device="cuda"), torch.ones(1, device="cuda")
+    assert torch.equal(ll.Int8LinearLayer.from_dense(W).forward(c, s).cpu(), torch.ones(1, 8, dtype=BF16))
