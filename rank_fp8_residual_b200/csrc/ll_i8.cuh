@@ -36,9 +36,9 @@ __device__ __forceinline__ void i8_settle() {
   while (clock_cycles() - c0 < kI8SettleCycles) {
   }
 }
-// The wait for the MMAs in flight (the barrier's only arrival is their commit's).
-__device__ __forceinline__ void i8_drain(uint64_t* bar, const Watch& w) {
-  mbar_wait_drain(bar, 0, Watch{w.status, max(w.timeout_ns, kI8SettleCycles / 2)});
+// The wait for MMAs or loads in flight, on the barrier that they complete on.
+__device__ __forceinline__ void i8_drain(uint64_t* bar, uint32_t parity, const Watch& w) {
+  mbar_wait_drain(bar, parity, Watch{w.status, max(w.timeout_ns, kI8SettleCycles / 2)});
 }
 
 // Two outputs from their sums: scaled by their tokens' scales sm, then s =
@@ -270,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       }
       // No MMA may still run when TMEM is released.
       commit_one_pair(drain, 0x1, one);
-      if (one) i8_drain(drain, p.watch);
+      if (one) i8_drain(drain, 0, p.watch);
       __syncwarp();
       done = ok;
     }
@@ -417,6 +417,9 @@ __host__ __device__ constexpr int is_smem_bytes(int Mt, int ring) {
 // and TMA stores by 16 epilogue warps, a launch for more than 32 tokens.  With one the int32 sums
 // go through shared memory ([token][feature]), and the CTAs of the cluster add
 // them over distributed shared memory, each for every splits-th token.
+//
+// 56 registers with 16 epilogue warps (8 have room for 102), so that the next
+// kernel's CTA fits beside one of the small ring.
 template <int kAct, int kEpiWarps>
 __global__ void __launch_bounds__(is_threads(kEpiWarps), kEpiWarps > 8 ? 2 : 1)
     ll_i8_stream_kernel(const __grid_constant__ I8StreamParams p) {
@@ -463,6 +466,7 @@ __global__ void __launch_bounds__(is_threads(kEpiWarps), kEpiWarps > 8 ? 2 : 1)
   pdl_launch_dependents();
   const uint32_t tbase = *tmem_slot;
   bool ok = true;
+  int issued = 0;  // K steps whose loads warp 0 has issued
   pdl_wait_primary();
 
   if (warp == 0) {
@@ -481,6 +485,7 @@ __global__ void __launch_bounds__(is_threads(kEpiWarps), kEpiWarps > 8 ? 2 : 1)
         load_2d_one(ring0 + slot * sb + 16384, &p.tm_x, full0 + 8u * slot, (s0 + i) * 128, 0, one);
         if (++slot == ns) { slot = 0; ph ^= 1; }
       }
+      issued = min(i, n);
     }
   } else if (warp == 1) {
     const uint32_t one = elect_one();
@@ -500,7 +505,7 @@ __global__ void __launch_bounds__(is_threads(kEpiWarps), kEpiWarps > 8 ? 2 : 1)
       if (++slot == ns) { slot = 0; ph ^= 1; }
     }
     commit_one(drain, one);
-    if (one) i8_drain(drain, p.watch);
+    if (one) i8_drain(drain, 0, p.watch);
     __syncwarp();
   } else {
     // TMEM lane = feature, column = token; the warps of a lane quadrant take
@@ -542,7 +547,8 @@ __global__ void __launch_bounds__(is_threads(kEpiWarps), kEpiWarps > 8 ? 2 : 1)
   }
   tc_fence_before();
   ok = __syncthreads_and(ok);
-  if (!ok && !p.withhold) i8_settle();  // loads that are in flight must land before the CTA exits
+  if (!ok && warp == 0)  // loads that are in flight must land before the CTA exits
+    for (int j = max(0, issued - ns); j < issued; ++j) i8_drain(&full[j % ns], (j / ns) & 1, p.watch);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tbase, p.tmem_cols);
